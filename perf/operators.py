@@ -12,7 +12,7 @@ import torch
 own = False
 
 GROUP = 32              # cache elements that share one scale
-TINY, HUGE = 2.0 ** -120, 2.0 ** 124   # the range of a scale
+TINY, HUGE = 2.0 ** -120, 2.0 ** 120   # the range of a scale
 
 
 # ---- sizes ------------------------------------------------------------------------------------------------------
@@ -78,6 +78,8 @@ def draw(rng):
     kv_top = _between(rng, 1, 100000 if kind == "one" else 4000)
     requests = _between(rng, 1, max(1, min(600, 60000000 // (kv_top * heads * d))))
     most = max(1, min(2000, 300000000 // (requests * kv_top * heads * share), 100000000 // (requests * heads * share * d)))
+    if kind == "causal":      # the cache holds the new events too
+        most = max(1, min(most, int((300000000 // (requests * heads * share)) ** 0.5)))
     q_top = 1 if kind == "one" else _between(rng, 1, min(40, most)) if kind == "few" else _between(rng, 1, most)
     return dict(op=op, requests=requests, page=page, heads=heads, share=share, d=d, kv=max(1, kv_top // 2), kv_top=kv_top, q=max(1, q_top // 2), q_top=q_top,
                 causal=kind == "causal", mix=mix)
