@@ -49,7 +49,8 @@ typedef enum {
   ROCS_ERR_WORKSPACE = 4,      /* workspace null or smaller than the *_workspace query */
   ROCS_ERR_INDEX = 5,          /* device: a request index outside [0, B_R); rows skipped */
   ROCS_ERR_DEVICE_TIMEOUT = 6, /* device: a bounded internal wait ran out; kernel returned */
-  ROCS_ERR_COUNTS = 7          /* device: counts negative or not summing to B_C */
+  ROCS_ERR_COUNTS = 7,         /* device: counts negative or not summing to B_C */
+  ROCS_ERR_VALUE = 8           /* device: an infinity or NaN where a finite value is stored */
 } rocs_status;
 
 typedef enum { ROCS_F32 = 0, ROCS_BF16 = 1 } rocs_dtype;
@@ -308,6 +309,130 @@ rocs_status rocs_dca_cross_attn_unsorted(rocs_handle_t handle, const void* Q, co
                                          int32_t H, int32_t d_h, float scale, void* O, int64_t ld_O,
                                          rocs_dtype out, const int32_t* kv_len, void* workspace,
                                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Paged 4-bit history cache.  A request's keys and values can outlive the call that made them: a
+ * user who comes back (or pages on) brings the same history plus some new events, and new events
+ * attend to what is cached.  The calls below keep keys and values in pages of 4-bit numbers, and a
+ * serving step is one of each, in this order, on one stream:
+ *   rocs_kv_block_tables     lengths -> pages, slots and positions of the new rows
+ *   rocs_qk_norm_rope        head norms and position rotation of the new queries and keys
+ *   rocs_kv4_append          new keys and values into their slots
+ *   rocs_dca_cross_attn_kv4  query rows (candidates, or the new events) against the cached history
+ * rocs_kv4_gather reads rows back as bf16 (for the dense rocs_dca_cross_attn, or to move pages).
+ * [REV] and [SUM] have no counterpart of the cache; the grouped attention is that of a9.
+ *
+ * Storage.  A cache of n_pages pages, page_size tokens each, is one buffer [n_pages, H_kv, record]
+ * of bytes, 16-byte aligned (rocs_kv4_cache_bytes in all).  The record of a page and head holds, one
+ * after the other: key codes [page_size, d_h / 2] bytes, key scales [page_size, d_h / 32] bf16, value
+ * codes, value scales.  Byte i of a row of codes holds elements 2i (low nibble) and 2i + 1; code n
+ * with its group's scale s (32 consecutive elements share one) is the value (n - 8) * s, n in 1..15.
+ * s is the smallest number of four significant bits that is no less than a 7th of the group's
+ * largest magnitude, within [2^-120, 2^120]; codes round to nearest, halves away from zero, and
+ * magnitudes beyond 7 * 2^120 saturate.  Every value (n - 8) * s is a bf16 number.
+ * Token t of request r lies in page block_table[r, t / page_size], at t % page_size; its slot is
+ * page * page_size + t % page_size.
+ * Limits: page_size 16, 32, 64 or 128; d_h 32, 64 or 128; 1 <= H_kv <= 1024; n_pages >= 1.
+ * Devices: these calls refuse (ROCS_ERR_INVALID_ARG) when the current device is not the handle's.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_pages, page_size, H_kv, d_h;
+} rocs_kv4_desc;
+
+rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc, size_t* bytes);
+
+/* Block tables and slot maps from request lengths, on the device.  Request r holds past_len[r]
+ * tokens and gets new_len[r] more; with P = page_size it takes
+ * ceil((past_len + new_len) / P) - ceil(past_len / P) pages from the front of free_pages, requests in
+ * order, and the new rows are numbered by request, then by position.
+ *   past_len, new_len [B_R] int32, device; past_len may be NULL (nothing is cached).
+ *   free_pages [n_free] int32, device (may be NULL with n_free = 0): distinct pages not in use.
+ *   block_table [B_R, max_blocks] int32, device, read and written: entries of the pages taken are
+ *            written, all others are left as they were.
+ *   kv_len  [B_R] int32, written: past_len + new_len.
+ *   row_offsets [B_R+1] int32, written: exclusive running total of new_len.
+ *   slots   [rows] int64, positions [rows] int32, written: each new row's slot and its position
+ *            past_len + j.  Rows behind the last request's (a padded batch) get -1 in both, which
+ *            the other calls skip.
+ *   pages_used [1] int32, written: how many entries of free_pages were taken.
+ * A request whose lengths are negative or exceed max_blocks * P tokens, or whose pages exceed what
+ * free_pages still holds, takes none: its rows (new_len of them, none if negative) get -1, its kv_len
+ * stays past_len (0 if past_len itself is unusable) and the device status becomes ROCS_ERR_COUNTS;
+ * new rows that sum to more than `rows` set it too (those beyond are not written).  A page outside
+ * [0, n_pages), in the table or the free list, gives its rows -1 and sets ROCS_ERR_INDEX.
+ * The outputs may not overlap the inputs or one another.
+ * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 4096
+ * requests), 16-byte aligned.  Limits: 1 <= B_R <= 2^24; 0 <= rows < 2^31 - 1; 0 <= n_free < 2^31 - 1;
+ * max_blocks >= 1 with max_blocks * P <= 2^31 - 256; page_size 16, 32, 64 or 128. */
+rocs_status rocs_kv_block_tables_workspace(rocs_handle_t handle, int32_t B_R, size_t* bytes);
+rocs_status rocs_kv_block_tables(rocs_handle_t handle, const int32_t* past_len, const int32_t* new_len, int32_t B_R,
+                                 int32_t page_size, const int32_t* free_pages, int32_t n_free, int32_t n_pages,
+                                 int32_t* block_table, int32_t max_blocks, int32_t* kv_len, int32_t* row_offsets,
+                                 int64_t* slots, int32_t* positions, int64_t rows, int32_t* pages_used,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* RMS norm of each query and key head, then the rotation of its first d_rot elements by the row's
+ * position, in one pass:
+ *   y_e = x_e / sqrt(mean_e(x_e^2) + eps) * gamma_e;
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s) for each pair t < d_rot / 2, with
+ *   c = cos_sin[position, t], s = cos_sin[position, d_rot / 2 + t] and (a, b) = (t, t + d_rot / 2), or
+ *   (2t, 2t + 1) with interleaved = 1.
+ *   Q [rows, H_q * d_h], K [rows, H_k * d_h] in `io` (bf16 or fp32), row strides ld_Q, ld_K elements:
+ *     they may be slices of one wider buffer.  H_q or H_k may be 0 (that side is ignored, its pointers
+ *     may be NULL).  Q_out, K_out in `io`, strides ld_Qo, ld_Ko; a side may be written in place (same
+ *     pointer and stride), else its output may not overlap the inputs.
+ *   gamma_q, gamma_k [d_h] fp32, or NULL for ones.  cos_sin [max_pos, d_rot] fp32 (cosines, then
+ *     sines), so that far positions' angles are as exact as the caller makes them.
+ *   positions [rows] int32, device: a row at -1 is padding, left as it was; any other position outside
+ *     [0, max_pos) is left as it was too and sets ROCS_ERR_INDEX.
+ * fp32 inside, one rounding.  Limits: d_h a multiple of 8, 16..256; d_rot a multiple of 16, 16..d_h;
+ * strides a multiple of 16 bytes; pointers 16-byte aligned; eps >= 0 and finite; 0 <= rows < 2^31. */
+typedef struct {
+  int64_t rows;
+  int32_t H_q, H_k, d_h, d_rot, interleaved, max_pos;
+  float eps;
+  rocs_dtype io;
+} rocs_qk_desc;
+
+rocs_status rocs_qk_norm_rope(rocs_handle_t handle, const rocs_qk_desc* desc, const void* Q, int64_t ld_Q,
+                              const void* K, int64_t ld_K, const float* gamma_q, const float* gamma_k,
+                              const float* cos_sin, const int32_t* positions, void* Q_out, int64_t ld_Qo,
+                              void* K_out, int64_t ld_Ko, void* stream);
+
+/* Keys and values to 4 bits in their slots (append), and back from their slots (gather).
+ *   K, V bf16 [rows, H_kv * d_h], row strides ld_K, ld_V elements (multiples of 8, pointers 16-byte
+ *     aligned).  slots [rows] int64, device: -1 skips the row (append writes nothing for it, gather
+ *     leaves its K and V as they were); another slot outside the cache is skipped and sets
+ *     ROCS_ERR_INDEX.  The slots of one append are distinct.
+ *   Append: a group with an infinity or a NaN is stored as zeros and sets ROCS_ERR_VALUE. */
+rocs_status rocs_kv4_append(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* K, int64_t ld_K,
+                            const void* V, int64_t ld_V, const int64_t* slots, int64_t rows, void* cache, void* stream);
+rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* cache, const int64_t* slots,
+                            int64_t rows, void* K, int64_t ld_K, void* V, int64_t ld_V, void* stream);
+
+/* a9 over the cache: grouped attention of query rows against their request's cached keys and values.
+ *   Q [rows, H_q * d_h] bf16, row stride ld_Q; H_q a multiple of H_kv, query head i reads key head
+ *     i / (H_q / H_kv).  Rows are grouped by request: offsets [B_R+1] int32, device.
+ *   block_table [B_R, max_blocks] int32, kv_len [B_R] int32, device: request r's keys are tokens
+ *     0 .. kv_len[r] - 1 (0 <= kv_len[r] <= max_blocks * page_size); entries past its last page are not
+ *     read.
+ *   causal = 0: every row sees all of its request's keys.  causal = 1: the request's n_r rows are its
+ *     last n_r tokens, so row i (from 0) sees the keys j <= kv_len[r] - n_r + i.
+ *   O [rows, H_q * d_h] bf16, row stride ld_O: softmax(q k^T * scale) v; a row that sees no key is 0.
+ * Scores, maxima, sums and outputs are accumulated in fp32; the weights enter the second product as
+ * bf16.  Offsets that decrease or leave [0, rows] set ROCS_ERR_INDEX, a kv_len outside its range
+ * ROCS_ERR_COUNTS: those requests' rows are not written.  A needed page outside [0, n_pages) sets
+ * ROCS_ERR_INDEX; its keys are left out.  Rows behind the last request's are left as they were.
+ * workspace: rocs_dca_cross_attn_kv4_workspace bytes (may be 0), 256-byte aligned.  Limits: strides
+ * multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256; rows * H_q < 2^31;
+ * 1 <= B_R <= 2^24; scale finite. */
+rocs_status rocs_dca_cross_attn_kv4_workspace(rocs_handle_t handle, const rocs_kv4_desc* desc, int32_t H_q,
+                                              int32_t B_R, int64_t rows, int32_t max_blocks, size_t* bytes);
+rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* Q, int64_t ld_Q,
+                                    int32_t H_q, const void* cache, const int32_t* block_table, int32_t max_blocks,
+                                    const int32_t* kv_len, const int32_t* offsets, int32_t B_R, int64_t rows,
+                                    float scale, int32_t causal, void* O, int64_t ld_O, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * a7. DCA shared sequence encoder and its K/V projections, request-only ([REV] §2.2:

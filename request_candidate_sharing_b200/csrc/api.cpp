@@ -818,6 +818,241 @@ extern "C" rocs_status rocs_dca_cross_attn_unsorted(rocs_handle_t h, const void*
 }
 
 // =============================================================================================
+// the paged 4-bit history cache
+// =============================================================================================
+namespace rocs {
+namespace {
+
+constexpr long long kMaxCachedTokens = 2147483647LL - 255;   // per request: token indexes stay int32 past the last chunk
+
+// The calls on the cache run on the handle's own device: a launch elsewhere would read its pointers
+// from the wrong GPU.
+rocs_status check_current_device(rocs_handle_t h, const char* who) {
+  int cur = -1;
+  ROCS_TRY(cuda_check(cudaGetDevice(&cur), "cudaGetDevice"));
+  ROCS_REQUIRE(cur == h->device, "%s: device %d is current, the handle's is %d", who, cur, h->device);
+  return ROCS_OK;
+}
+
+bool good_page_size(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+rocs_status check_kv4_desc(const rocs_kv4_desc* d, const char* who) {
+  ROCS_REQUIRE(d != nullptr, "%s: desc is NULL", who);
+  ROCS_REQUIRE(d->n_pages >= 1, "%s: n_pages=%d must be >= 1", who, d->n_pages);
+  ROCS_REQUIRE(good_page_size(d->page_size), "%s: page_size=%d (16, 32, 64 or 128 supported)", who, d->page_size);
+  ROCS_REQUIRE(d->H_kv >= 1 && d->H_kv <= 1024, "%s: H_kv=%d out of range", who, d->H_kv);
+  ROCS_REQUIRE(d->d_h == 32 || d->d_h == 64 || d->d_h == 128, "%s: d_h=%d (32, 64 or 128 supported)", who, d->d_h);
+  return ROCS_OK;
+}
+
+// Whether [a, a + na) and [b, b + nb) bytes share any.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+rocs_status check_kv4_rows(const rocs_kv4_desc* d, const void* K, int64_t ld_K, const void* V, int64_t ld_V,
+                           const int64_t* slots, int64_t rows, const void* cache, const char* who) {
+  ROCS_TRY(check_kv4_desc(d, who));
+  ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL, "%s: rows=%lld out of range", who, (long long)rows);
+  ROCS_REQUIRE(cache && (rows == 0 || (K && V && slots)), "%s: NULL argument", who);
+  const int64_t width = (int64_t)d->H_kv * d->d_h;
+  ROCS_REQUIRE(ld_K >= width && ld_V >= width && ld_K % 8 == 0 && ld_V % 8 == 0,
+               "%s: row strides must be multiples of 8, at least H_kv * d_h", who);
+  ROCS_REQUIRE(aligned16(K) && aligned16(V) && aligned16(cache) && ((uintptr_t)slots & 7) == 0, "%s: misaligned", who);
+  return ROCS_OK;
+}
+
+rocs_status check_attn_kv4(const rocs_kv4_desc* d, int32_t H_q, int32_t B_R, int64_t rows, int32_t max_blocks) {
+  const char* who = "rocs_dca_cross_attn_kv4";
+  ROCS_TRY(check_kv4_desc(d, who));
+  ROCS_REQUIRE(H_q >= 1 && H_q % d->H_kv == 0, "%s: H_q=%d must be a multiple of H_kv=%d", who, H_q, d->H_kv);
+  ROCS_REQUIRE(B_R >= 1 && B_R <= (1 << 24), "%s: B_R=%d out of range", who, B_R);
+  ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL / H_q, "%s: rows=%lld times H_q out of range", who, (long long)rows);
+  ROCS_REQUIRE(max_blocks >= 1 && (long long)max_blocks * d->page_size <= kMaxCachedTokens,
+               "%s: max_blocks=%d out of range", who, max_blocks);
+  return ROCS_OK;
+}
+
+}  // namespace
+}  // namespace rocs
+
+extern "C" rocs_status rocs_kv4_cache_bytes(rocs_handle_t h, const rocs_kv4_desc* d, size_t* bytes) {
+  ROCS_REQUIRE(h && bytes, "rocs_kv4_cache_bytes: NULL argument");
+  ROCS_TRY(check_kv4_desc(d, "rocs_kv4_cache_bytes"));
+  *bytes = (size_t)d->n_pages * d->H_kv * ((size_t)d->page_size * d->d_h * 9 / 8);
+  return ROCS_OK;
+}
+
+extern "C" rocs_status rocs_kv_block_tables_workspace(rocs_handle_t h, int32_t B_R, size_t* bytes) {
+  ROCS_REQUIRE(h && bytes, "rocs_kv_block_tables_workspace: NULL argument");
+  ROCS_REQUIRE(B_R >= 1 && B_R <= (1 << 24), "rocs_kv_block_tables_workspace: B_R=%d out of range", B_R);
+  *bytes = kv_tables_scratch(B_R);
+  return ROCS_OK;
+}
+
+extern "C" rocs_status rocs_kv_block_tables(rocs_handle_t h, const int32_t* past_len, const int32_t* new_len,
+                                            int32_t B_R, int32_t page_size, const int32_t* free_pages,
+                                            int32_t n_free, int32_t n_pages, int32_t* block_table,
+                                            int32_t max_blocks, int32_t* kv_len, int32_t* row_offsets, int64_t* slots,
+                                            int32_t* positions, int64_t rows, int32_t* pages_used, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  CtxGuard ctx_guard_(h);
+  const char* who = "rocs_kv_block_tables";
+  ROCS_REQUIRE(h, "%s: handle is NULL", who);
+  ROCS_REQUIRE(new_len && block_table && kv_len && row_offsets && pages_used, "%s: NULL argument", who);
+  ROCS_REQUIRE(B_R >= 1 && B_R <= (1 << 24), "%s: B_R=%d out of range", who, B_R);
+  ROCS_REQUIRE(good_page_size(page_size), "%s: page_size=%d (16, 32, 64 or 128 supported)", who, page_size);
+  ROCS_REQUIRE(n_free >= 0 && n_free < 2147483647 && (free_pages || n_free == 0), "%s: bad free list", who);
+  ROCS_REQUIRE(n_pages >= 1, "%s: n_pages=%d must be >= 1", who, n_pages);
+  ROCS_REQUIRE(max_blocks >= 1 && (long long)max_blocks * page_size <= kMaxCachedTokens,
+               "%s: max_blocks=%d out of range", who, max_blocks);
+  ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL && (rows == 0 || (slots && positions)), "%s: bad rows", who);
+  ROCS_REQUIRE(aligned16(slots) && aligned16(positions), "%s: slots and positions must be 16-byte aligned", who);
+  const void* out[] = {block_table, kv_len, row_offsets, slots, positions, pages_used};
+  const size_t n_out[] = {(size_t)B_R * max_blocks * 4, (size_t)B_R * 4, (size_t)B_R * 4 + 4, (size_t)rows * 8,
+                          (size_t)rows * 4, 4};
+  const void* in[] = {past_len, new_len, free_pages};
+  const size_t n_in[] = {(size_t)B_R * 4, (size_t)B_R * 4, (size_t)n_free * 4};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = 0; j < 3; ++j)
+      ROCS_REQUIRE(!overlap(out[i], n_out[i], in[j], n_in[j]), "%s: an output overlaps an input", who);
+    for (int j = 0; j < i; ++j)
+      ROCS_REQUIRE(!overlap(out[i], n_out[i], out[j], n_out[j]), "%s: two outputs overlap", who);
+  }
+  const size_t need = kv_tables_scratch(B_R);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) {
+    set_error("%s: workspace of %zu bytes (16-byte aligned) needed", who, need);
+    return ROCS_ERR_WORKSPACE;
+  }
+  ROCS_TRY(check_current_device(h, who));
+  return launch_kv_tables(h, past_len, new_len, B_R, 31 - __builtin_clz((unsigned)page_size), free_pages, n_free,
+                          n_pages, block_table, max_blocks, kv_len, row_offsets, slots, positions, rows, pages_used,
+                          workspace, (cudaStream_t)stream);
+}
+
+extern "C" rocs_status rocs_qk_norm_rope(rocs_handle_t h, const rocs_qk_desc* d, const void* Q, int64_t ld_Q,
+                                         const void* K, int64_t ld_K, const float* gamma_q, const float* gamma_k,
+                                         const float* cos_sin, const int32_t* positions, void* Q_out, int64_t ld_Qo,
+                                         void* K_out, int64_t ld_Ko, void* stream) {
+  CtxGuard ctx_guard_(h);
+  const char* who = "rocs_qk_norm_rope";
+  ROCS_REQUIRE(h && d, "%s: NULL argument", who);
+  ROCS_REQUIRE(d->rows >= 0 && d->rows < 2147483647LL, "%s: rows=%lld out of range", who, (long long)d->rows);
+  ROCS_REQUIRE(d->io == ROCS_F32 || d->io == ROCS_BF16, "%s: bad dtype", who);
+  ROCS_REQUIRE(d->H_q >= 0 && d->H_k >= 0 && d->H_q <= 4096 && d->H_k <= 4096 && d->H_q + d->H_k >= 1,
+               "%s: bad head counts", who);
+  ROCS_REQUIRE(d->d_h >= 16 && d->d_h <= 256 && d->d_h % 8 == 0, "%s: d_h=%d (a multiple of 8, 16..256)", who, d->d_h);
+  ROCS_REQUIRE(d->d_rot >= 16 && d->d_rot <= d->d_h && d->d_rot % 16 == 0,
+               "%s: d_rot=%d (a multiple of 16, 16..d_h)", who, d->d_rot);
+  ROCS_REQUIRE(d->interleaved == 0 || d->interleaved == 1, "%s: bad interleaved", who);
+  ROCS_REQUIRE(d->max_pos >= 1, "%s: max_pos=%d must be >= 1", who, d->max_pos);
+  ROCS_REQUIRE(std::isfinite(d->eps) && d->eps >= 0.f, "%s: eps must be finite and >= 0", who);
+  const int esz = d->io == ROCS_F32 ? 4 : 2;
+  struct Side { const void* x; int64_t ld; void* y; int64_t ldo; int32_t H; const float* g; };
+  const Side sides[2] = {{Q, ld_Q, Q_out, ld_Qo, d->H_q, gamma_q}, {K, ld_K, K_out, ld_Ko, d->H_k, gamma_k}};
+  if (d->rows > 0) ROCS_REQUIRE(cos_sin && positions, "%s: NULL argument", who);
+  ROCS_REQUIRE(aligned16(cos_sin) && ((uintptr_t)positions & 3) == 0, "%s: misaligned", who);
+  for (int i = 0; i < 2; ++i) {
+    const Side& s = sides[i];
+    if (s.H == 0) continue;
+    ROCS_REQUIRE(d->rows == 0 || (s.x && s.y), "%s: NULL argument", who);
+    const int64_t width = (int64_t)s.H * d->d_h;
+    ROCS_REQUIRE(s.ld >= width && s.ldo >= width && s.ld * esz % 16 == 0 && s.ldo * esz % 16 == 0,
+                 "%s: row strides must be multiples of 16 bytes, at least the heads' width", who);
+    ROCS_REQUIRE(aligned16(s.x) && aligned16(s.y) && aligned16(s.g), "%s: misaligned", who);
+    // a side in place reads each unit before it writes it; the other side, or a shifted copy of its
+    // own, might be read after.  Two interleaved slices of one buffer do not overlap, though their
+    // spans do: those are told apart by their columns when the strides agree.
+    if (d->rows == 0) continue;
+    for (int j = 0; j < 2; ++j) {
+      const Side& o = sides[j];
+      if (o.H == 0 || (i == j && s.x == s.y && s.ld == s.ldo)) continue;
+      const int64_t wj = (int64_t)o.H * d->d_h;
+      const size_t ny = ((size_t)(d->rows - 1) * s.ldo + width) * esz, nx = ((size_t)(d->rows - 1) * o.ld + wj) * esz;
+      if (!overlap(s.y, ny, o.x, nx)) continue;
+      bool apart = false;
+      if (s.ldo == o.ld) {
+        const int64_t period = s.ldo * esz;
+        int64_t at = ((int64_t)((uintptr_t)o.x - (uintptr_t)s.y)) % period;
+        if (at < 0) at += period;
+        apart = at >= width * esz && at + wj * esz <= period;
+      }
+      ROCS_REQUIRE(apart, "%s: an output overlaps an input", who);
+    }
+  }
+  if (d->H_q > 0 && d->H_k > 0 && d->rows > 0) {
+    const int64_t wq = (int64_t)d->H_q * d->d_h, wk = (int64_t)d->H_k * d->d_h;
+    bool clash = overlap(Q_out, ((size_t)(d->rows - 1) * ld_Qo + wq) * esz, K_out, ((size_t)(d->rows - 1) * ld_Ko + wk) * esz);
+    if (clash && ld_Qo == ld_Ko) {
+      const int64_t period = ld_Qo * esz;
+      int64_t at = ((int64_t)((uintptr_t)K_out - (uintptr_t)Q_out)) % period;
+      if (at < 0) at += period;
+      clash = !(at >= wq * esz && at + wk * esz <= period);
+    }
+    ROCS_REQUIRE(!clash, "%s: the two outputs overlap", who);
+  }
+  ROCS_TRY(check_current_device(h, who));
+  return launch_qk_norm_rope(h, *d, Q, ld_Q, K, ld_K, gamma_q, gamma_k, cos_sin, positions, Q_out, ld_Qo, K_out,
+                             ld_Ko, (cudaStream_t)stream);
+}
+
+extern "C" rocs_status rocs_kv4_append(rocs_handle_t h, const rocs_kv4_desc* d, const void* K, int64_t ld_K,
+                                       const void* V, int64_t ld_V, const int64_t* slots, int64_t rows, void* cache,
+                                       void* stream) {
+  CtxGuard ctx_guard_(h);
+  ROCS_REQUIRE(h, "rocs_kv4_append: handle is NULL");
+  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, "rocs_kv4_append"));
+  ROCS_TRY(check_current_device(h, "rocs_kv4_append"));
+  return launch_kv4_append(h, *d, K, ld_K, V, ld_V, slots, rows, cache, (cudaStream_t)stream);
+}
+
+extern "C" rocs_status rocs_kv4_gather(rocs_handle_t h, const rocs_kv4_desc* d, const void* cache,
+                                       const int64_t* slots, int64_t rows, void* K, int64_t ld_K, void* V,
+                                       int64_t ld_V, void* stream) {
+  CtxGuard ctx_guard_(h);
+  ROCS_REQUIRE(h, "rocs_kv4_gather: handle is NULL");
+  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, "rocs_kv4_gather"));
+  ROCS_TRY(check_current_device(h, "rocs_kv4_gather"));
+  return launch_kv4_gather(h, *d, cache, slots, rows, K, ld_K, V, ld_V, (cudaStream_t)stream);
+}
+
+extern "C" rocs_status rocs_dca_cross_attn_kv4_workspace(rocs_handle_t h, const rocs_kv4_desc* d, int32_t H_q,
+                                                         int32_t B_R, int64_t rows, int32_t max_blocks,
+                                                         size_t* bytes) {
+  ROCS_REQUIRE(h && bytes, "rocs_dca_cross_attn_kv4_workspace: NULL argument");
+  ROCS_TRY(check_attn_kv4(d, H_q, B_R, rows, max_blocks));
+  *bytes = attn_kv4_scratch(h, *d, H_q, B_R, rows, max_blocks);
+  return ROCS_OK;
+}
+
+extern "C" rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t h, const rocs_kv4_desc* d, const void* Q, int64_t ld_Q,
+                                               int32_t H_q, const void* cache, const int32_t* block_table,
+                                               int32_t max_blocks, const int32_t* kv_len, const int32_t* offsets,
+                                               int32_t B_R, int64_t rows, float scale, int32_t causal, void* O,
+                                               int64_t ld_O, void* workspace, size_t workspace_bytes, void* stream) {
+  CtxGuard ctx_guard_(h);
+  const char* who = "rocs_dca_cross_attn_kv4";
+  ROCS_REQUIRE(h, "%s: handle is NULL", who);
+  ROCS_TRY(check_attn_kv4(d, H_q, B_R, rows, max_blocks));
+  ROCS_REQUIRE(cache && block_table && kv_len && offsets && (rows == 0 || (Q && O)), "%s: NULL argument", who);
+  const int64_t width = (int64_t)H_q * d->d_h;
+  ROCS_REQUIRE(ld_Q >= width && ld_O >= width && ld_Q % 8 == 0 && ld_O % 8 == 0,
+               "%s: row strides must be multiples of 8, at least H_q * d_h", who);
+  ROCS_REQUIRE(aligned16(Q) && aligned16(O) && aligned16(cache), "%s: misaligned", who);
+  ROCS_REQUIRE(std::isfinite(scale), "%s: scale not finite", who);
+  ROCS_REQUIRE(causal == 0 || causal == 1, "%s: causal must be 0 or 1", who);
+  const size_t need = attn_kv4_scratch(h, *d, H_q, B_R, rows, max_blocks);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255))) {
+    set_error("%s: workspace of %zu bytes (256-byte aligned) needed", who, need);
+    return ROCS_ERR_WORKSPACE;
+  }
+  ROCS_TRY(check_current_device(h, who));
+  return launch_attn_kv4(h, *d, Q, ld_Q, H_q, cache, block_table, max_blocks, kv_len, offsets, B_R, rows, scale,
+                         causal, O, ld_O, workspace, (cudaStream_t)stream);
+}
+
+// =============================================================================================
 // a7
 // =============================================================================================
 namespace rocs {

@@ -1,0 +1,594 @@
+// Grouped attention over the 4-bit paged history cache, for few query rows per request.
+//
+//   O_i = sum_j softmax_j(scale q_i . k_j) v_j   over the keys j that row i sees,
+// with k_j, v_j = (code - 8) * scale dequantised in registers (exactly: see kv4.cuh).
+//
+// The share query heads of a key head are packed with the request's query rows into tiles of 8 NT
+// rows, and the products are taken transposed on m16n8k16 MMAs (S^T = K Q^T, O^T = V^T P^T): the
+// cache is the 16-row operand, which comes straight from the packed words, and one to eight query
+// rows waste no more than an 8-wide tile.  The contraction index of either product may be permuted
+// at will as long as both operands agree, so
+//   S^T: a lane takes whole words of a key's row (d / 32 neighbouring ones), whose nibbles (0, 4),
+//        (1, 5), (2, 6), (3, 7) are the bf16 pairs; the queries are loaded in that order once;
+//   O^T: a lane takes the word of its eight output elements from four keys, and pairs equal nibbles
+//        of two keys; rows rho = 0..7 of a score tile are the keys (rho >> 1) + 4 (rho & 1), so that
+//        the words of the lanes' first keys lie side by side (no bank conflicts up to d = 64).
+// P^T moves from the accumulator's layout to the operand's by an 8x8 transpose in registers.
+//
+// Bound by the cache's bytes.  A block of four warps has the keys of one (tile, head, split); each
+// warp streams its own 64-key chunks through a ring of bulk copies and keeps its own running
+// maximum, sum and output, joined through shared memory at the end, so the loop has no block-wide
+// wait.  Where the (tile, head) items are too few to fill the GPU the keys are split over blocks,
+// whose partial results a second launch joins in a fixed order.
+#include <float.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "mma_frag.cuh"
+
+namespace rocs {
+namespace {
+
+constexpr int KA_WARPS = 4;
+constexpr int KA_CHUNK = 64;    // keys per stage of a warp's ring
+
+template <int D>
+struct KaCfg {
+  static constexpr int STAGE = KA_CHUNK * D * 9 / 8;
+  static constexpr int STAGES = D == 32 ? 4 : D == 64 ? 3 : 2;
+  static constexpr int RING = STAGE * STAGES;
+  static constexpr int SMEM = KA_WARPS * RING;
+};
+
+struct KaParams {
+  const __nv_bfloat16* Q;
+  long long ldq;
+  const uint8_t* cache;
+  const int32_t* table;
+  int max_blocks;
+  const int32_t *kv_len, *offsets;
+  int B_R;
+  long long rows;
+  int Hkv, share, P_log2, n_pages;
+  float sl2;            // |scale| * log2(e), at least the smallest normal number
+  uint32_t q_flip;      // sign bits to flip in a query pair (a negative scale)
+  int causal;
+  __nv_bfloat16* O;
+  long long ldo;
+  int n_split;
+  float* part;          // [tile][head][split][row][D] sums, then [tile][head][split][row] (max, sum) pairs
+  float2* part_ml;
+  int* status;
+};
+
+// The request of tile t: request r's tiles start at floor(offsets[r] * share / T) + r, which leaves
+// room for ceil(n_r * share / T) of them without another pass over the counts.  Every lane of the
+// calling warp gets the answer (32 probes a step).
+__device__ __forceinline__ long long ka_tile_start(const KaParams& p, int r, int T) {
+  long long o = p.offsets[r];
+  o = o < 0 ? 0 : o > p.rows ? p.rows : o;
+  return o * p.share / T + r;
+}
+__device__ __forceinline__ int ka_request(const KaParams& p, long long t, int T) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.B_R;   // start(lo) <= t; the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int r = lo + lane * step;
+    const bool le = r < hi && (lane == 0 || ka_tile_start(p, r, T) <= t);
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int k = m == 0xffffffffu ? 31 : __ffs((int)~m) - 2;   // lanes 0..k hold
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+struct KaTile {
+  int r, n, first;       // request, its packed rows (n_r * share), the tile's first packed row
+  long long q0;          // the request's first query row
+  int len, n_r;          // keys, query rows
+};
+
+// Geometry of tile t; false where there is nothing to do.
+__device__ __forceinline__ bool ka_tile(const KaParams& p, long long t, int T, KaTile& a) {
+  a.r = ka_request(p, t, T);
+  const long long q0 = p.offsets[a.r], q1 = p.offsets[a.r + 1];
+  a.len = p.kv_len[a.r];
+  if (q0 < 0 || q1 < q0 || q1 > p.rows || a.len < 0 || a.len > ((long long)p.max_blocks << p.P_log2)) return false;
+  const long long ti = t - ka_tile_start(p, a.r, T), n = (q1 - q0) * p.share;
+  if (ti < 0 || ti * T >= n) return false;
+  a.q0 = q0;
+  a.n_r = (int)(q1 - q0);
+  a.n = (int)n;
+  a.first = (int)(ti * T);
+  return true;
+}
+
+// Keys that packed row m of the tile's request sees: [0, limit).
+__device__ __forceinline__ int ka_limit(const KaParams& p, const KaTile& a, int m) {
+  return p.causal ? max(0, a.len - a.n_r + m / p.share + 1) : a.len;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int N>
+__device__ __forceinline__ void ka_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams p) {
+  using C = KaCfg<D>;
+  constexpr int T = 8 * NT;
+  constexpr int KW = D / 32;                  // words of a key row per lane (scores)
+  constexpr int VW = D >= 64 ? D / 64 : 1;    // words of a key row per lane (values)
+  constexpr int VN = D >= 64 ? 4 : 2;         // 16-row output tiles per word
+  constexpr int MT = VW * VN;                 // = D / 16
+  extern __shared__ __align__(128) uint8_t ka_smem[];
+  __shared__ uint64_t bars[KA_WARPS][C::STAGES];
+  __shared__ float s_m[KA_WARPS][T], s_l[KA_WARPS][T];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3;
+  const int h = blockIdx.y;
+
+  // every request's lengths are looked at once, whether a tile reads them or not
+  if (blockIdx.y == 0 && blockIdx.z == 0) {
+    const long long r = (long long)blockIdx.x * (KA_WARPS * 32) + threadIdx.x;
+    if (r < p.B_R) {
+      const long long q0 = p.offsets[r], q1 = p.offsets[r + 1], len = p.kv_len[r];
+      if (q0 < 0 || q1 < q0 || q1 > p.rows) set_status(p.status, ROCS_ERR_INDEX);
+      if (len < 0 || len > ((long long)p.max_blocks << p.P_log2)) set_status(p.status, ROCS_ERR_COUNTS);
+    }
+  }
+  KaTile a;
+  if (!ka_tile(p, blockIdx.x, T, a)) return;
+  const int last = min(a.first + T, a.n) - 1;       // last packed row of the tile
+  const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
+  const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
+  const int chunks = (seen + KA_CHUNK - 1) / KA_CHUNK;
+  const int c_lo = (int)((long long)chunks * blockIdx.z / p.n_split);
+  const int c_hi = (int)((long long)chunks * (blockIdx.z + 1) / p.n_split);
+
+  uint8_t* ring = ka_smem + warp * C::RING;
+  if (lane == 0)
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars[warp][i], 1);
+  fence_barrier_init();
+  fence_proxy_async_smem();
+  __syncwarp();
+
+  // a chunk's pages: pieces of PE = min(page, 64) keys, each a record of PE keys in the stage
+  const int PE_log2 = min(p.P_log2, 6), PE = 1 << PE_log2;
+  const int pieces = KA_CHUNK >> PE_log2;
+  const int rec = kv4_record_bytes(PE, D);
+  const int32_t* table = p.table + (long long)a.r * p.max_blocks;
+  auto page_of = [&](int c) -> int {      // lane i < pieces: the page of piece i of chunk c (-2: none is needed)
+    const long long key = (long long)c * KA_CHUNK + ((long long)lane << PE_log2);
+    return lane < pieces && c < c_hi && key < a.len ? table[key >> p.P_log2] : -2;
+  };
+  uint32_t bad_of = 0;                    // 4 bits per stage: pieces whose page does not exist
+  auto issue = [&](int c, int st, int page) {
+    const bool ok = page >= 0 && page < p.n_pages;
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    const uint32_t bad = __ballot_sync(0xffffffffu, !ok && page != -2);
+    bad_of = (bad_of & ~(15u << (4 * st))) | ((bad & 15u) << (4 * st));
+    if (bad != 0 && lane == 0) set_status(p.status, ROCS_ERR_INDEX);
+    uint64_t* bar = &bars[warp][st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mask) * rec));
+    __syncwarp();
+    if (ok) {
+      uint8_t* dst = ring + st * C::STAGE + lane * rec;
+      const long long P = 1LL << p.P_log2;
+      const uint8_t* src = p.cache + ((long long)page * p.Hkv + h) * kv4_record_bytes((int)P, D);
+      if (p.P_log2 <= 6) {
+        bulk_load(dst, src, rec, bar);
+      } else {                            // half of a 128-token page: its four parts one by one
+        const int o = (c & 1) * KA_CHUNK;
+        constexpr int CB = kv4_codes_bytes(KA_CHUNK, D), SB = kv4_scales_bytes(KA_CHUNK, D);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint8_t* half = src + v * kv4_half_bytes((int)P, D);
+          bulk_load(dst + v * (CB + SB), half + kv4_codes_bytes(o, D), CB, bar);
+          bulk_load(dst + v * (CB + SB) + CB, half + kv4_codes_bytes((int)P, D) + kv4_scales_bytes(o, D), SB, bar);
+        }
+      }
+    }
+  };
+
+  // the queries, in the order of the keys' nibble pairs
+  uint32_t qf[NT][KW][4];
+  int limit[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int m = a.first + nt * 8 + g;
+    const bool live = m < a.n;
+    const __nv_bfloat16* q = p.Q + (a.q0 + m / p.share) * p.ldq + ((long long)h * p.share + m % p.share) * D;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (live) x = *reinterpret_cast<const uint4*>(q + (tq * KW + w) * 8);
+      qf[nt][w][0] = __byte_perm(x.x, x.z, 0x5410) ^ p.q_flip;   // (0, 4)
+      qf[nt][w][1] = __byte_perm(x.x, x.z, 0x7632) ^ p.q_flip;   // (1, 5)
+      qf[nt][w][2] = __byte_perm(x.y, x.w, 0x5410) ^ p.q_flip;   // (2, 6)
+      qf[nt][w][3] = __byte_perm(x.y, x.w, 0x7632) ^ p.q_flip;   // (3, 7)
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) limit[nt][e] = ka_limit(p, a, min(a.first + nt * 8 + 2 * tq + e, a.n - 1));
+  }
+
+  float o[MT][NT][4];
+  float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m_run[nt][0] = m_run[nt][1] = -INFINITY;
+    l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+  }
+
+  // the warp's chunks: c_lo + warp, then every fourth; the ring is filled ahead, page numbers one
+  // chunk further ahead still
+  int c_issue = c_lo + warp;
+  int st_issue = 0;
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) {
+    if (c_issue < c_hi) {
+      issue(c_issue, st_issue, page_of(c_issue));
+      c_issue += KA_WARPS;
+      ++st_issue;
+    }
+  }
+  int next_page = page_of(c_issue);
+  if (st_issue == C::STAGES) st_issue = 0;
+  int st = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  const int key_row = (g >> 1) + 4 * (g & 1);
+  for (int c = c_lo + warp; c < c_hi; c += KA_WARPS) {
+    if (c_issue < c_hi) {     // into the stage read in the last turn
+      __syncwarp();
+      issue(c_issue, st_issue, next_page);
+      if (++st_issue == C::STAGES) st_issue = 0;
+      c_issue += KA_WARPS;
+      next_page = page_of(c_issue);
+    }
+    // after a wait that ran out, what is in flight is still waited for, then the warp leaves
+    alive = __all_sync(0xffffffffu, mbar_wait(&bars[warp][st], phase, p.status, nullptr)) && alive;
+    if (alive) {
+      const uint8_t* stage = ring + st * C::STAGE;
+      const int k0 = c * KA_CHUNK;
+      const uint32_t bad = (bad_of >> (4 * st)) & 15u;
+      const bool whole = bad == 0 && k0 + KA_CHUNK <= sees_all && k0 + KA_CHUNK <= a.len;
+      float s[4][NT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int piece = (16 * t) >> PE_log2, in = (16 * t) & (PE - 1);
+        const uint8_t* base = stage + piece * rec;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[t][nt][0] = s[t][nt][1] = s[t][nt][2] = s[t][nt][3] = 0.f;
+        uint32_t w0[KW], w1[KW];
+        const int r0 = in + key_row;
+        ka_words<KW>(base + r0 * (D / 2) + tq * (4 * KW), w0);
+        ka_words<KW>(base + (r0 + 8) * (D / 2) + tq * (4 * KW), w1);
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(base + kv4_codes_bytes(PE, D));
+        const int grp = (tq * KW) >> 2;
+        uint32_t s0 = sc[r0 * (D / 32) + grp], s1 = sc[(r0 + 8) * (D / 32) + grp];
+        s0 |= s0 << 16;
+        s1 |= s1 << 16;
+        const uint32_t f0 = kv4_offset(s0), f1 = kv4_offset(s1);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t e0[4], e1[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e0[i] = kv4_fma2(kv4_pair(w0[w] >> (4 * i)), s0, f0);
+            e1[i] = kv4_fma2(kv4_pair(w1[w] >> (4 * i)), s1, f1);
+          }
+          const uint32_t a0[4] = {e0[0], e1[0], e0[1], e1[1]}, a1[4] = {e0[2], e1[2], e0[3], e1[3]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(s[t][nt], a0, qf[nt][w][0], qf[nt][w][1]);
+            mma_bf16_16816(s[t][nt], a1, qf[nt][w][2], qf[nt][w][3]);
+          }
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bool lost = (bad >> ((16 * t) >> PE_log2)) & 1u;
+          const int j = k0 + 16 * t + key_row;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (lost || j + 8 * (e >> 1) >= limit[nt][e & 1]) s[t][nt][e] = -INFINITY;
+        }
+      }
+      // running maximum and sum of each query column; P^T in the operand's layout
+      uint32_t pf[4][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+          for (int t = 1; t < 4; ++t) mx[e] = fmaxf(mx[e], fmaxf(s[t][nt][e], s[t][nt][e + 2]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
+        }
+        float neg[2], corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m_new = fmaxf(m_run[nt][e], mx[e] * p.sl2);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;    // nothing seen yet: every exponential is 0
+          corr[e] = ex2_approx(m_run[nt][e] - ref);
+          neg[e] = -ref;
+          m_run[nt][e] = m_new;
+          l_run[nt][e] *= corr[e];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) e4[e] = ex2_approx(fmaf(s[t][nt][e], p.sl2, neg[e & 1]));
+          l_run[nt][0] += e4[0] + e4[2];
+          l_run[nt][1] += e4[1] + e4[3];
+          pf[t][nt][0] = transpose8x8(pack_bf16x2(e4[0], e4[1]));
+          pf[t][nt][1] = transpose8x8(pack_bf16x2(e4[2], e4[3]));
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int piece = (16 * t) >> PE_log2, in = (16 * t) & (PE - 1);
+        const uint8_t* base = stage + piece * rec + kv4_half_bytes(PE, D);
+        const int word = D >= 64 ? g * VW : (g & 3), grp = word >> 2;
+        const int pre = D >= 64 ? 0 : 8 * (g >> 2);    // d = 32: lanes 4 apart share a word
+        uint32_t vw[4][VW], vs[4];
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(base + kv4_codes_bytes(PE, D));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = in + tq + 4 * i;
+          ka_words<VW>(base + r * (D / 2) + word * 4, vw[i]);
+          vs[i] = sc[r * (D / 32) + grp];
+        }
+        if (!whole) {
+          // a key that does not exist has a weight of zero, but what lies in its place may be
+          // anything: its value is made zero too
+          const bool lost = (bad >> piece) & 1u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (lost || k0 + 16 * t + tq + 4 * i >= a.len) vs[i] = 0;
+        }
+        const uint32_t sa = vs[0] | (vs[1] << 16), sb = vs[2] | (vs[3] << 16);
+        const uint32_t fa = kv4_offset(sa), fb = kv4_offset(sb);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t la = __byte_perm(vw[0][w], vw[1][w], 0x5410) >> pre, ha = __byte_perm(vw[0][w], vw[1][w], 0x7632) >> pre;
+          const uint32_t lb = __byte_perm(vw[2][w], vw[3][w], 0x5410) >> pre, hb = __byte_perm(vw[2][w], vw[3][w], 0x7632) >> pre;
+#pragma unroll
+          for (int i = 0; i < VN; ++i) {
+            const uint32_t av[4] = {kv4_fma2(kv4_pair(la >> (4 * i)), sa, fa), kv4_fma2(kv4_pair(ha >> (4 * i)), sa, fa),
+                                    kv4_fma2(kv4_pair(lb >> (4 * i)), sb, fb), kv4_fma2(kv4_pair(hb >> (4 * i)), sb, fb)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[w * VN + i][nt], av, pf[t][nt][0], pf[t][nt][1]);
+          }
+        }
+      }
+    }
+    if (++st == C::STAGES) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+
+  // join the warps: outputs through the ring's memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = l_run[nt][e];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+      if (g == 0) {
+        s_m[warp][nt * 8 + 2 * tq + e] = m_run[nt][e];
+        s_l[warp][nt * 8 + 2 * tq + e] = l;
+      }
+    }
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(ka_smem);        // [warp][row][D]
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int w = mt / VN, i = mt % VN;
+    const int d0 = D >= 64 ? 8 * (g * VW + w) + i : 8 * (g & 3) + 2 * (g >> 2) + i;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        so[(warp * T + nt * 8 + 2 * tq + (e & 1)) * D + d0 + 4 * (e >> 1)] = o[mt][nt][e];
+  }
+  __syncthreads();
+  const long long item = ((long long)blockIdx.x * p.Hkv + h) * p.n_split + blockIdx.z;
+  for (int i = threadIdx.x; i < T * (D / 2); i += KA_WARPS * 32) {
+    const int row = i / (D / 2), d = 2 * (i % (D / 2));
+    const int m = a.first + row;
+    if (m >= a.n) break;
+    float top = s_m[0][row];
+#pragma unroll
+    for (int w = 1; w < KA_WARPS; ++w) top = fmaxf(top, s_m[w][row]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < KA_WARPS; ++w) {
+      const float f = ex2_approx(s_m[w][row] - ref);
+      const float2 v = *reinterpret_cast<const float2*>(so + (w * T + row) * D + d);
+      l = fmaf(f, s_l[w][row], l);
+      x = fmaf(f, v.x, x);
+      y = fmaf(f, v.y, y);
+    }
+    if (p.n_split == 1) {
+      const float inv = l == 0.f ? 0.f : 1.0f / l;      // a row that sees nothing is zero
+      __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
+      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
+    } else {
+      *reinterpret_cast<float2*>(p.part + (item * T + row) * D + d) = make_float2(x, y);
+      if (d == 0) p.part_ml[item * T + row] = make_float2(top, l);
+    }
+  }
+}
+
+// Joins the splits of each (tile, head), in order.
+template <int D, int T>
+__global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p) {
+  KaTile a;
+  if (!ka_tile(p, blockIdx.x, T, a)) return;
+  const int h = blockIdx.y;
+  const long long item0 = ((long long)blockIdx.x * p.Hkv + h) * p.n_split;
+  for (int i = threadIdx.x; i < T * (D / 2); i += 128) {
+    const int row = i / (D / 2), d = 2 * (i % (D / 2));
+    const int m = a.first + row;
+    if (m >= a.n) break;
+    float top = -INFINITY;
+    for (int s = 0; s < p.n_split; ++s) top = fmaxf(top, p.part_ml[(item0 + s) * T + row].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f, x = 0.f, y = 0.f;
+    for (int s = 0; s < p.n_split; ++s) {
+      const float2 ml = p.part_ml[(item0 + s) * T + row];
+      const float2 v = *reinterpret_cast<const float2*>(p.part + ((item0 + s) * T + row) * D + d);
+      const float f = ex2_approx(ml.x - ref);
+      l = fmaf(f, ml.y, l);
+      x = fmaf(f, v.x, x);
+      y = fmaf(f, v.y, y);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
+  }
+}
+
+// How a call is laid out: rows per tile, an upper bound of its tiles, and the key splits.
+struct KaPlan {
+  int NT = 1, T = 8, n_split = 1;
+  long long tiles = 0;
+  size_t part_bytes = 0, bytes = 0;
+};
+
+KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R, long long rows, int max_blocks) {
+  KaPlan k;
+  const int share = H_q / d.H_kv;
+  const long long packed = rows * share;
+  // as many packed rows per tile as a request has on average, within the registers
+  const double avg = (double)packed / B_R;
+  k.NT = avg <= 8 ? 1 : avg <= 16 || d.d_h == 128 ? 2 : 4;
+  k.T = 8 * k.NT;
+  k.tiles = packed / k.T + B_R;
+  // fill about twice the resident blocks (four an SM); a split has at least four chunks a warp
+  const long long busy = (packed + k.T - 1) / k.T;
+  const long long items = (busy < 1 ? 1 : busy) * d.H_kv;
+  const long long want = 8LL * ctx->num_sms;
+  const long long longest = ((long long)max_blocks * d.page_size + KA_CHUNK - 1) / KA_CHUNK;
+  long long split = items >= want / 2 ? 1 : want / items;
+  const long long most = longest / (4 * KA_WARPS);
+  split = split > most ? most : split;
+  k.n_split = (int)(split < 1 ? 1 : split > 1024 ? 1024 : split);
+  if (k.n_split > 1) {
+    const size_t n = (size_t)k.tiles * d.H_kv * k.n_split * k.T;
+    k.part_bytes = (n * d.d_h * 4 + 255) / 256 * 256;
+    k.bytes = k.part_bytes + n * 8;
+  }
+  return k;
+}
+
+template <int D, int NT>
+rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  using C = KaCfg<D>;
+  static_assert(C::SMEM >= KA_WARPS * 8 * NT * D * 4, "the join's outputs fit the ring");
+  static bool attr[64] = {false};
+  if (C::SMEM > 48 * 1024 && (ctx->device >= 64 || !attr[ctx->device])) {
+    rocs_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     C::SMEM), "cudaFuncSetAttribute(attn_kv4)");
+    if (st != ROCS_OK) return st;
+    if (ctx->device < 64) attr[ctx->device] = true;
+  }
+  {
+    LaunchTimer lt_("attn_kv4", s);
+    attn_kv4_kernel<D, NT><<<dim3((unsigned)k.tiles, p.Hkv, k.n_split), KA_WARPS * 32, C::SMEM, s>>>(p);
+  }
+  if (k.n_split > 1) {
+    LaunchTimer lt_("attn_kv4_join", s);
+    attn_kv4_join_kernel<D, 8 * NT><<<dim3((unsigned)k.tiles, p.Hkv), 128, 0, s>>>(p);
+  }
+  return cuda_check(cudaGetLastError(), "attn_kv4_kernel");
+}
+
+template <int D>
+rocs_status ka_dispatch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  if (k.NT == 1) return ka_launch<D, 1>(ctx, p, k, s);
+  if (k.NT == 2) return ka_launch<D, 2>(ctx, p, k, s);
+  if constexpr (D < 128) return ka_launch<D, 4>(ctx, p, k, s);
+  return ROCS_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+size_t attn_kv4_scratch(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R, long long rows, int max_blocks) {
+  return ka_plan(ctx, d, H_q, B_R, rows, max_blocks).bytes;
+}
+
+rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const void* Q, long long ldq, int H_q,
+                            const void* cache, const int32_t* table, int max_blocks, const int32_t* kv_len,
+                            const int32_t* offsets, int B_R, long long rows, float scale, int causal, void* O,
+                            long long ldo, void* scratch, cudaStream_t s) {
+  if (rows == 0) return ROCS_OK;
+  const KaPlan k = ka_plan(ctx, d, H_q, B_R, rows, max_blocks);
+  KaParams p;
+  p.Q = (const __nv_bfloat16*)Q;
+  p.ldq = ldq;
+  p.cache = (const uint8_t*)cache;
+  p.table = table;
+  p.max_blocks = max_blocks;
+  p.kv_len = kv_len;
+  p.offsets = offsets;
+  p.B_R = B_R;
+  p.rows = rows;
+  p.Hkv = d.H_kv;
+  p.share = H_q / d.H_kv;
+  p.P_log2 = 31 - __builtin_clz((unsigned)d.page_size);
+  p.n_pages = d.n_pages;
+  // a negative scale turns the queries round, so that the largest product is the largest score
+  p.sl2 = fmaxf(fabsf(scale) * 1.4426950408889634f, FLT_MIN);
+  p.q_flip = scale < 0.f ? 0x80008000u : 0u;
+  p.causal = causal;
+  p.O = (__nv_bfloat16*)O;
+  p.ldo = ldo;
+  p.n_split = k.n_split;
+  p.part = (float*)scratch;
+  p.part_ml = (float2*)((char*)scratch + k.part_bytes);
+  p.status = ctx->d_status;
+  switch (d.d_h) {
+    case 32: return ka_dispatch<32>(ctx, p, k, s);
+    case 64: return ka_dispatch<64>(ctx, p, k, s);
+    default: return ka_dispatch<128>(ctx, p, k, s);
+  }
+}
+
+}  // namespace rocs

@@ -253,6 +253,30 @@ rocs_status launch_attention_tc(rocs_context* ctx, const void* Q, long long ldq,
                                 const int32_t* out_rows = nullptr, const int32_t* kv_len = nullptr,
                                 int q_by_kv = 0, const int32_t* order = nullptr);
 
+// The 4-bit history cache.  Block tables and slot maps (kv_tables.cu): scratch of
+// kv_tables_scratch(B_R) bytes (0 up to 4096 requests).
+size_t kv_tables_scratch(int B_R);
+rocs_status launch_kv_tables(rocs_context* ctx, const int32_t* past, const int32_t* fresh_len, int B_R, int page_log2,
+                             const int32_t* free_pages, int n_free, int n_pages, int32_t* table, int max_blocks,
+                             int32_t* kv_len, int32_t* row_off, int64_t* slots, int32_t* positions, long long rows,
+                             int32_t* pages_used, void* scratch, cudaStream_t s);
+// Head norms and rotation (qk_rope.cu).
+rocs_status launch_qk_norm_rope(rocs_context* ctx, const rocs_qk_desc& d, const void* Q, long long ldq, const void* K,
+                                long long ldk, const float* gq, const float* gk, const float* table,
+                                const int32_t* pos, void* Qo, long long ldqo, void* Ko, long long ldko,
+                                cudaStream_t s);
+// Rows of keys and values into their slots, and back (kv4_cache.cu).
+rocs_status launch_kv4_append(rocs_context* ctx, const rocs_kv4_desc& d, const void* K, long long ldk, const void* V,
+                              long long ldv, const int64_t* slots, long long rows, void* cache, cudaStream_t s);
+rocs_status launch_kv4_gather(rocs_context* ctx, const rocs_kv4_desc& d, const void* cache, const int64_t* slots,
+                              long long rows, void* K, long long ldk, void* V, long long ldv, cudaStream_t s);
+// Grouped attention over the cache (attn_kv4.cu); scratch of attn_kv4_scratch bytes, 256-byte aligned.
+size_t attn_kv4_scratch(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R, long long rows, int max_blocks);
+rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const void* Q, long long ldq, int H_q,
+                            const void* cache, const int32_t* table, int max_blocks, const int32_t* kv_len,
+                            const int32_t* offsets, int B_R, long long rows, float scale, int causal, void* O,
+                            long long ldo, void* scratch, cudaStream_t s);
+
 // Exponentials per second of the attention softmax's per-score steps with n_poly of every eight
 // pairs on the FMA-pipe polynomial (probe.cu); synchronises s.
 rocs_status probe_exp2_rate(rocs_context* ctx, int n_poly, double* rate, cudaStream_t s);

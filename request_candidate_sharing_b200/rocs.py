@@ -20,13 +20,13 @@ _lib = C.CDLL(LIB_PATH)
 
 # ---- enums ----
 ROCS_OK, ROCS_ERR_INVALID_ARG, ROCS_ERR_UNSUPPORTED, ROCS_ERR_CUDA = 0, 1, 2, 3
-ROCS_ERR_WORKSPACE, ROCS_ERR_INDEX, ROCS_ERR_DEVICE_TIMEOUT, ROCS_ERR_COUNTS = 4, 5, 6, 7
+ROCS_ERR_WORKSPACE, ROCS_ERR_INDEX, ROCS_ERR_DEVICE_TIMEOUT, ROCS_ERR_COUNTS, ROCS_ERR_VALUE = 4, 5, 6, 7, 8
 ROCS_F32, ROCS_BF16 = 0, 1
 ACT = {"none": 0, "relu": 1, "gelu": 2, "sigmoid": 3}
 MAX_LAYERS = 8
 
 STATUS_NAMES = {0: "ROCS_OK", 1: "ROCS_ERR_INVALID_ARG", 2: "ROCS_ERR_UNSUPPORTED", 3: "ROCS_ERR_CUDA",
-                4: "ROCS_ERR_WORKSPACE", 5: "ROCS_ERR_INDEX", 6: "ROCS_ERR_DEVICE_TIMEOUT", 7: "ROCS_ERR_COUNTS"}
+                4: "ROCS_ERR_WORKSPACE", 5: "ROCS_ERR_INDEX", 6: "ROCS_ERR_DEVICE_TIMEOUT", 7: "ROCS_ERR_COUNTS", 8: "ROCS_ERR_VALUE"}
 
 P = C.c_void_p
 I32 = C.c_int32
@@ -43,6 +43,15 @@ class RocsError(RuntimeError):
 class IkboDesc(C.Structure):
     _fields_ = [("B_R", I32), ("B_C", I64), ("d_R_in", I32), ("d_C_in", I32), ("d_R_out", I32),
                 ("d_C_out", I32), ("dtype_in", C.c_int), ("dtype_out", C.c_int), ("act", C.c_int)]
+
+
+class Kv4Desc(C.Structure):
+    _fields_ = [("n_pages", I32), ("page_size", I32), ("H_kv", I32), ("d_h", I32)]
+
+
+class QkDesc(C.Structure):
+    _fields_ = [("rows", I64), ("H_q", I32), ("H_k", I32), ("d_h", I32), ("d_rot", I32), ("interleaved", I32),
+                ("max_pos", I32), ("eps", C.c_float), ("io", C.c_int)]
 
 
 class DcaLayerWeights(C.Structure):
@@ -136,6 +145,16 @@ _lib_sort = _proto("rocs_sort_by_request", P, P, I32, I64, P, P, P, C.c_size_t, 
 _lib_xu_ws = _proto("rocs_dca_cross_attn_unsorted_workspace", P, I32, I64, I32, I32, C.c_int, C.POINTER(C.c_size_t))
 _lib_xu = _proto("rocs_dca_cross_attn_unsorted", P, P, P, P, P, I32, I64, I32, I32, I32, C.c_float, P, I64, C.c_int, P,
                  P, C.c_size_t, P)
+_lib_kv4_bytes = _proto("rocs_kv4_cache_bytes", P, C.POINTER(Kv4Desc), C.POINTER(C.c_size_t))
+_lib_tab_ws = _proto("rocs_kv_block_tables_workspace", P, I32, C.POINTER(C.c_size_t))
+_lib_tab = _proto("rocs_kv_block_tables", P, P, P, I32, I32, P, I32, I32, P, I32, P, P, P, P, I64, P, P, C.c_size_t, P)
+_lib_qk = _proto("rocs_qk_norm_rope", P, C.POINTER(QkDesc), P, I64, P, I64, P, P, P, P, P, I64, P, I64, P)
+_lib_kv4_app = _proto("rocs_kv4_append", P, C.POINTER(Kv4Desc), P, I64, P, I64, P, I64, P, P)
+_lib_kv4_get = _proto("rocs_kv4_gather", P, C.POINTER(Kv4Desc), P, P, I64, P, I64, P, I64, P)
+_lib_attn4_ws = _proto("rocs_dca_cross_attn_kv4_workspace", P, C.POINTER(Kv4Desc), I32, I32, I64, I32,
+                       C.POINTER(C.c_size_t))
+_lib_attn4 = _proto("rocs_dca_cross_attn_kv4", P, C.POINTER(Kv4Desc), P, I64, I32, P, P, I32, P, P, I32, I64, C.c_float,
+                    I32, P, I64, P, C.c_size_t, P)
 _lib_partition = _proto("rocs_partition_requests", P, I32, I32, C.c_double, C.c_double, P)
 _lib_tstart = _proto("rocs_timing_start", P, I32)
 _lib_tstop = _proto("rocs_timing_stop", P, C.c_char_p, C.c_size_t)
@@ -147,7 +166,9 @@ EXPORTED = ["rocs_linear_ikbo_noalloc", "rocs_timing_start", "rocs_timing_stop",
             "rocs_set_graph_replay", "rocs_set_ikbo_fused", "rocs_test_withhold_ikbo_flag", "rocs_probe_exp2_rate", "rocs_set_w8_tensor_cores", "rocs_sort_by_request_workspace",
             "rocs_sort_by_request", "rocs_dca_cross_attn_unsorted_workspace", "rocs_dca_cross_attn_unsorted",
             "rocs_quantize_weights_fp8", "rocs_linear_ikbo_w8_workspace", "rocs_linear_ikbo_w8",
-            "rocs_partition_requests"]
+            "rocs_partition_requests", "rocs_kv4_cache_bytes", "rocs_kv_block_tables_workspace", "rocs_kv_block_tables",
+            "rocs_qk_norm_rope", "rocs_kv4_append", "rocs_kv4_gather", "rocs_dca_cross_attn_kv4_workspace",
+            "rocs_dca_cross_attn_kv4"]
 
 
 def ptr(x) -> Optional[int]:
@@ -357,6 +378,52 @@ class Rocs:
         _check(_lib_xu(self.h, ptr(Q), ptr(K), ptr(V), ptr(req_idx), int(B_R), int(rows), int(L), int(H), int(d_h),
                        float(scale), ptr(O), int(ld_O), int(out), ptr(kv_len), ptr(workspace), int(workspace_bytes),
                        stream))
+
+
+    # -- paged 4-bit history cache --
+    def rocs_kv4_cache_bytes(self, desc: Kv4Desc) -> int:
+        n = C.c_size_t(0)
+        _check(_lib_kv4_bytes(self.h, C.byref(desc), C.byref(n)))
+        return int(n.value)
+
+    def rocs_kv_block_tables_workspace(self, B_R: int) -> int:
+        n = C.c_size_t(0)
+        _check(_lib_tab_ws(self.h, int(B_R), C.byref(n)))
+        return int(n.value)
+
+    def rocs_kv_block_tables(self, past_len, new_len, B_R: int, page_size: int, free_pages, n_free: int, n_pages: int,
+                             block_table, max_blocks: int, kv_len, row_offsets, slots, positions, rows: int, pages_used,
+                             workspace, workspace_bytes: int, stream=None):
+        """past_len: tokens each request holds (device int32 [B_R]), or None where nothing is cached."""
+        _check(_lib_tab(self.h, ptr(past_len), ptr(new_len), int(B_R), int(page_size), ptr(free_pages), int(n_free),
+                        int(n_pages), ptr(block_table), int(max_blocks), ptr(kv_len), ptr(row_offsets), ptr(slots),
+                        ptr(positions), int(rows), ptr(pages_used), ptr(workspace), int(workspace_bytes), stream))
+
+    def rocs_qk_norm_rope(self, desc: QkDesc, Q, ld_Q: int, K, ld_K: int, gamma_q, gamma_k, cos_sin, positions, Q_out,
+                          ld_Qo: int, K_out, ld_Ko: int, stream=None):
+        _check(_lib_qk(self.h, C.byref(desc), ptr(Q), int(ld_Q), ptr(K), int(ld_K), ptr(gamma_q), ptr(gamma_k),
+                       ptr(cos_sin), ptr(positions), ptr(Q_out), int(ld_Qo), ptr(K_out), int(ld_Ko), stream))
+
+    def rocs_kv4_append(self, desc: Kv4Desc, K, ld_K: int, V, ld_V: int, slots, rows: int, cache, stream=None):
+        _check(_lib_kv4_app(self.h, C.byref(desc), ptr(K), int(ld_K), ptr(V), int(ld_V), ptr(slots), int(rows),
+                            ptr(cache), stream))
+
+    def rocs_kv4_gather(self, desc: Kv4Desc, cache, slots, rows: int, K, ld_K: int, V, ld_V: int, stream=None):
+        _check(_lib_kv4_get(self.h, C.byref(desc), ptr(cache), ptr(slots), int(rows), ptr(K), int(ld_K), ptr(V),
+                            int(ld_V), stream))
+
+    def rocs_dca_cross_attn_kv4_workspace(self, desc: Kv4Desc, H_q: int, B_R: int, rows: int, max_blocks: int) -> int:
+        n = C.c_size_t(0)
+        _check(_lib_attn4_ws(self.h, C.byref(desc), int(H_q), int(B_R), int(rows), int(max_blocks), C.byref(n)))
+        return int(n.value)
+
+    def rocs_dca_cross_attn_kv4(self, desc: Kv4Desc, Q, ld_Q: int, H_q: int, cache, block_table, max_blocks: int, kv_len,
+                                offsets, B_R: int, rows: int, scale: float, causal: int, O, ld_O: int, workspace,
+                                workspace_bytes: int, stream=None):
+        """causal: 1 where the query rows are their request's last tokens and see up to themselves."""
+        _check(_lib_attn4(self.h, C.byref(desc), ptr(Q), int(ld_Q), int(H_q), ptr(cache), ptr(block_table),
+                          int(max_blocks), ptr(kv_len), ptr(offsets), int(B_R), int(rows), float(scale), int(causal),
+                          ptr(O), int(ld_O), ptr(workspace), int(workspace_bytes), stream))
 
 
 # ---- marshalling helpers for the model structs (names follow the synth weight dictionaries) ----
