@@ -17,8 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librocs.so")
 
 SOURCES = ["api.cpp", "gemm_tc.cu", "misc.cu", "layernorm.cu", "fm.cu", "attention.cu", "attn_stream.cu", "attn_tc.cu", "attn_req.cu", "noalloc.cu", "sort.cu", "w8.cu", "w8_tc.cu", "probe.cu",
-           "kv_tables.cu", "qk_rope.cu", "kv4_cache.cu", "attn_kv4.cu"]
-HEADERS = ["common.cuh", "internal.h", "mma_frag.cuh", "softmax_math.cuh", "kv4.cuh"]
+           "kv_tables.cu", "qk_rope.cu", "kv4_cache.cu", "attn_kv4.cu", "attn_kv4_tc.cu"]
+HEADERS = ["common.cuh", "internal.h", "mma_frag.cuh", "softmax_math.cuh", "kv4.cuh", "attn_kv4.cuh", "tc_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", os.path.join(ROOT, "include")]

@@ -22,6 +22,7 @@
 // whose partial results a second launch joins in a fixed order.
 #include <float.h>
 
+#include "attn_kv4.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -31,6 +32,7 @@ namespace rocs {
 namespace {
 
 constexpr int KA_WARPS = 4;
+constexpr int kTcRows = 32;     // packed rows a request above which the 128-row tensor-core tiles pay
 constexpr int KA_CHUNK = 64;    // keys per stage of a warp's ring
 
 template <int D>
@@ -40,76 +42,6 @@ struct KaCfg {
   static constexpr int RING = STAGE * STAGES;
   static constexpr int SMEM = KA_WARPS * RING;
 };
-
-struct KaParams {
-  const __nv_bfloat16* Q;
-  long long ldq;
-  const uint8_t* cache;
-  const int32_t* table;
-  int max_blocks;
-  const int32_t *kv_len, *offsets;
-  int B_R;
-  long long rows;
-  int Hkv, share, P_log2, n_pages;
-  float sl2;            // |scale| * log2(e), at least the smallest normal number
-  uint32_t q_flip;      // sign bits to flip in a query pair (a negative scale)
-  int causal;
-  __nv_bfloat16* O;
-  long long ldo;
-  int n_split;
-  float* part;          // [tile][head][split][row][D] sums, then [tile][head][split][row] (max, sum) pairs
-  float2* part_ml;
-  int* status;
-};
-
-// The request of tile t: request r's tiles start at floor(offsets[r] * share / T) + r, which leaves
-// room for ceil(n_r * share / T) of them without another pass over the counts.  Every lane of the
-// calling warp gets the answer (32 probes a step).
-__device__ __forceinline__ long long ka_tile_start(const KaParams& p, int r, int T) {
-  long long o = p.offsets[r];
-  o = o < 0 ? 0 : o > p.rows ? p.rows : o;
-  return o * p.share / T + r;
-}
-__device__ __forceinline__ int ka_request(const KaParams& p, long long t, int T) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.B_R;   // start(lo) <= t; the answer is in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int r = lo + lane * step;
-    const bool le = r < hi && (lane == 0 || ka_tile_start(p, r, T) <= t);
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    const int k = m == 0xffffffffu ? 31 : __ffs((int)~m) - 2;   // lanes 0..k hold
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-struct KaTile {
-  int r, n, first;       // request, its packed rows (n_r * share), the tile's first packed row
-  long long q0;          // the request's first query row
-  int len, n_r;          // keys, query rows
-};
-
-// Geometry of tile t; false where there is nothing to do.
-__device__ __forceinline__ bool ka_tile(const KaParams& p, long long t, int T, KaTile& a) {
-  a.r = ka_request(p, t, T);
-  const long long q0 = p.offsets[a.r], q1 = p.offsets[a.r + 1];
-  a.len = p.kv_len[a.r];
-  if (q0 < 0 || q1 < q0 || q1 > p.rows || a.len < 0 || a.len > ((long long)p.max_blocks << p.P_log2)) return false;
-  const long long ti = t - ka_tile_start(p, a.r, T), n = (q1 - q0) * p.share;
-  if (ti < 0 || ti * T >= n) return false;
-  a.q0 = q0;
-  a.n_r = (int)(q1 - q0);
-  a.n = (int)n;
-  a.first = (int)(ti * T);
-  return true;
-}
-
-// Keys that packed row m of the tile's request sees: [0, limit).
-__device__ __forceinline__ int ka_limit(const KaParams& p, const KaTile& a, int m) {
-  return p.causal ? max(0, a.len - a.n_r + m / p.share + 1) : a.len;
-}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -144,15 +76,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3;
   const int h = blockIdx.y;
 
-  // every request's lengths are looked at once, whether a tile reads them or not
-  if (blockIdx.y == 0 && blockIdx.z == 0) {
-    const long long r = (long long)blockIdx.x * (KA_WARPS * 32) + threadIdx.x;
-    if (r < p.B_R) {
-      const long long q0 = p.offsets[r], q1 = p.offsets[r + 1], len = p.kv_len[r];
-      if (q0 < 0 || q1 < q0 || q1 > p.rows) set_status(p.status, ROCS_ERR_INDEX);
-      if (len < 0 || len > ((long long)p.max_blocks << p.P_log2)) set_status(p.status, ROCS_ERR_COUNTS);
-    }
-  }
+  if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
   KaTile a;
   if (!ka_tile(p, blockIdx.x, T, a)) return;
   const int last = min(a.first + T, a.n) - 1;       // last packed row of the tile
@@ -487,7 +411,7 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p) {
 
 // How a call is laid out: rows per tile, an upper bound of its tiles, and the key splits.
 struct KaPlan {
-  int NT = 1, T = 8, n_split = 1;
+  int NT = 1, T = 8, n_split = 1;   // NT = 0: the tcgen05 kernel
   long long tiles = 0;
   size_t part_bytes = 0, bytes = 0;
 };
@@ -496,18 +420,18 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   KaPlan k;
   const int share = H_q / d.H_kv;
   const long long packed = rows * share;
-  // as many packed rows per tile as a request has on average, within the registers
+  // as many packed rows per tile as a request has on average
   const double avg = (double)packed / B_R;
-  k.NT = avg <= 8 ? 1 : avg <= 16 || d.d_h == 128 ? 2 : 4;
-  k.T = 8 * k.NT;
+  k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
+  k.T = k.NT > 0 ? 8 * k.NT : 128;
   k.tiles = packed / k.T + B_R;
   // fill about twice the resident blocks (four an SM); a split has at least four chunks a warp
   const long long busy = (packed + k.T - 1) / k.T;
   const long long items = (busy < 1 ? 1 : busy) * d.H_kv;
-  const long long want = 8LL * ctx->num_sms;
+  const long long want = (k.NT > 0 ? 8LL : 4LL) * ctx->num_sms;
   const long long longest = ((long long)max_blocks * d.page_size + KA_CHUNK - 1) / KA_CHUNK;
   long long split = items >= want / 2 ? 1 : want / items;
-  const long long most = longest / (4 * KA_WARPS);
+  const long long most = longest / (k.NT > 0 ? 4 * KA_WARPS : 8);
   split = split > most ? most : split;
   k.n_split = (int)(split < 1 ? 1 : split > 1024 ? 1024 : split);
   if (k.n_split > 1) {
@@ -516,6 +440,13 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
     k.bytes = k.part_bytes + n * 8;
   }
   return k;
+}
+
+template <int D, int T>
+rocs_status ka_join(const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  LaunchTimer lt_("attn_kv4_join", s);
+  attn_kv4_join_kernel<D, T><<<dim3((unsigned)k.tiles, p.Hkv), 128, 0, s>>>(p);
+  return cuda_check(cudaGetLastError(), "attn_kv4_join_kernel");
 }
 
 template <int D, int NT>
@@ -533,15 +464,17 @@ rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cud
     LaunchTimer lt_("attn_kv4", s);
     attn_kv4_kernel<D, NT><<<dim3((unsigned)k.tiles, p.Hkv, k.n_split), KA_WARPS * 32, C::SMEM, s>>>(p);
   }
-  if (k.n_split > 1) {
-    LaunchTimer lt_("attn_kv4_join", s);
-    attn_kv4_join_kernel<D, 8 * NT><<<dim3((unsigned)k.tiles, p.Hkv), 128, 0, s>>>(p);
-  }
-  return cuda_check(cudaGetLastError(), "attn_kv4_kernel");
+  rocs_status st = cuda_check(cudaGetLastError(), "attn_kv4_kernel");
+  return st != ROCS_OK || k.n_split == 1 ? st : ka_join<D, 8 * NT>(p, k, s);
 }
 
 template <int D>
 rocs_status ka_dispatch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  if (k.NT == 0) {
+    rocs_status st = launch_attn_kv4_tc(ctx, D, p, k.tiles, s);
+    if (st != ROCS_OK || k.n_split == 1) return st;
+    return ka_join<D, 128>(p, k, s);
+  }
   if (k.NT == 1) return ka_launch<D, 1>(ctx, p, k, s);
   if (k.NT == 2) return ka_launch<D, 2>(ctx, p, k, s);
   if constexpr (D < 128) return ka_launch<D, 4>(ctx, p, k, s);

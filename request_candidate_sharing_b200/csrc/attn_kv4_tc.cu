@@ -1,0 +1,426 @@
+// Grouped attention over the 4-bit paged history cache, for many query rows per request, on the
+// 5th-generation tensor cores.
+//
+// One CTA takes 128 packed rows (query row x shared head) of one request against one key head, in
+// blocks of 64 keys; two CTAs share an SM, so that one's start and end hide behind the other.
+//   warps 0-3  softmax, one thread per row (TMEM lane): S is read from tensor memory, its maximum
+//              and exponentials are taken in registers (three pairs in eight on the FMA pipe), and P
+//              is written back over S as bf16 pairs, the A operand of P V.  The row's reference
+//              maximum moves only when a block exceeds it by more than 2^8.
+//   warps 4-7  producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
+//              value at a time, a block ahead in registers, dequantises it (exactly) and writes it as
+//              bf16 into the operand's swizzled tile in shared memory.  The conversion is paid once
+//              per 128 rows; a copy of the codes through shared memory would only lengthen the way.
+//   warp 4     also issues the MMAs, between two blocks' conversions: S_j = Q K_j^T into one of two
+//              buffers, O += P_j V_j.  They execute in order, so S_{j+1} is in flight while the softmax
+//              works on S_j, and the P in a buffer is consumed before the S two blocks later lands on
+//              it.  (A warp of its own for them would cost every thread a fifth of its registers.)
+// Codes come out of a word as the pairs (0, 4), (1, 5), (2, 6), (3, 7); keys and queries keep that
+// order (a contraction index may be permuted), and the output's columns are put right as they are
+// stored.  Bound by the exponentials; all waits are bounded (ROCS_ERR_DEVICE_TIMEOUT), after which
+// the CTA drains its MMAs, releases tensor memory and returns.
+#include "attn_kv4.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "softmax_math.cuh"
+#include "tc_attn.cuh"
+
+namespace rocs {
+namespace {
+
+constexpr int KT_ROWS = 128;
+constexpr int KT_KEYS = 64;
+constexpr int KT_THREADS = 256;
+constexpr float kKtLazyLog2 = 8.0f;
+
+template <int D>
+struct KtCfg {
+  static constexpr int PANELS = D == 128 ? 2 : 1;          // swizzled panels of at most 64 elements
+  static constexpr int ROWB = D == 32 ? 64 : 128;          // bytes of a panel's row
+  static constexpr uint32_t SW = D == 32 ? 4u : 2u;        // 64- or 128-byte swizzle
+  static constexpr uint32_t SBO = 8 * ROWB;
+  static constexpr int Q_PANEL = KT_ROWS * ROWB, KV_PANEL = KT_KEYS * ROWB;
+  static constexpr int Q_BYTES = PANELS * Q_PANEL, KV_BYTES = PANELS * KV_PANEL;   // of K, and of V
+  static constexpr int STAGES = D == 32 ? 4 : D == 64 ? 3 : 2;
+  static constexpr int S_COL = 0, O_COL = 2 * KT_KEYS, TMEM_COLS = 256;
+  static constexpr int USED = Q_BYTES + 2 * STAGES * KV_BYTES + 1024;
+  // two CTAs an SM, never three: a third could not have its tensor memory
+  static constexpr int SMEM = USED > 80 * 1024 ? USED : 80 * 1024;
+  static constexpr int UNITS = KT_KEYS * (D / KV4_GROUP) * 2 / 128;   // groups per producer thread and block
+};
+
+// Byte offset of 16-byte unit c (of the whole row of D elements) of row r in a swizzled tile.
+template <int D>
+__device__ __forceinline__ uint32_t kt_unit(int r, int c, int panel_bytes) {
+  if constexpr (D == 32) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)((c >> 3) * panel_bytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Eight elements of a row in the codes' order (0, 4, 1, 5, 2, 6, 3, 7).
+__device__ __forceinline__ uint4 kt_order(uint4 x) {
+  return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                    __byte_perm(x.y, x.w, 0x7632));
+}
+
+template <int D>
+__global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaParams p) {
+  using C = KtCfg<D>;
+  constexpr uint32_t IDESC_S = idesc_bf16(KT_ROWS, KT_KEYS, false);
+  constexpr uint32_t IDESC_O = idesc_bf16(KT_ROWS, D == 128 ? 64 : D, true);
+  extern __shared__ uint8_t kt_raw[];
+  __shared__ uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], q_full, s_full[2], p_full[2], pv_done[2], drain;
+  __shared__ uint32_t s_bad[8];            // per block (mod 8): 16-key pieces whose page does not exist
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kt_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = base;
+  uint8_t* sKV = base + C::Q_BYTES;        // [STAGES][K | V]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y;
+
+  if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
+  KaTile a;
+  if (!ka_tile(p, blockIdx.x, KT_ROWS, a)) return;
+  const int last = min(a.first + KT_ROWS, a.n) - 1;
+  const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
+  const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
+  const int blocks = (seen + KT_KEYS - 1) / KT_KEYS;
+  const int b_lo = (int)((long long)blocks * blockIdx.z / p.n_split);
+  const int n = (int)((long long)blocks * (blockIdx.z + 1) / p.n_split) - b_lo;
+
+  if (threadIdx.x < 8) s_bad[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&kv_full[i], 128);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(&q_full, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < 4) {
+    // ---------------- softmax: thread = row = TMEM lane ----------------
+    const int row = threadIdx.x;
+    const int m = a.first + row;
+    const bool live = m < a.n;
+    const long long qrow = a.q0 + m / p.share;
+    const long long col = ((long long)h * p.share + m % p.share) * D;
+    {
+      const __nv_bfloat16* q = p.Q + qrow * p.ldq + col;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (live) x = kt_order(*reinterpret_cast<const uint4*>(q + 8 * c));
+        x.x ^= p.q_flip; x.y ^= p.q_flip; x.z ^= p.q_flip; x.w ^= p.q_flip;
+        *reinterpret_cast<uint4*>(sQ + kt_unit<D>(row, c, C::Q_PANEL)) = x;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full);
+    }
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const bool warp_live = a.first + warp * 32 < a.n;      // rows past the request's end are not computed
+    const int limit = live ? ka_limit(p, a, m) : 0;
+    const float sl2 = p.sl2;
+    float m_cur = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int b = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], (j >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t saddr = lane_addr + C::S_COL + b * KT_KEYS;
+      if (warp_live) {
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(saddr, v[0]);
+        tmem_ld_32x32b_x32(saddr + 32, v[1]);
+        tmem_ld_wait();
+        const int k0 = (b_lo + j) * KT_KEYS;
+        const uint32_t bad = *(volatile uint32_t*)&s_bad[j & 7];
+        const bool masked = bad != 0 || k0 + KT_KEYS > sees_all;
+        if (masked) {
+          const int valid = limit - k0;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e >= valid || ((bad >> (e >> 4)) & 1u)) v[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+        }
+        float mt[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mt[t] = fmaxf(__uint_as_float(v[0][t]), __uint_as_float(v[0][t + 8]));
+#pragma unroll
+        for (int e = 16; e < 64; e += 16)
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            mt[t] = fmax3(mt[t], __uint_as_float(v[(e + t) >> 5][(e + t) & 31]), __uint_as_float(v[(e + 8 + t) >> 5][(e + 8 + t) & 31]));
+        const float mx = fmax3(fmax3(mt[0], mt[1], mt[2]), fmax3(mt[3], mt[4], mt[5]), fmaxf(mt[6], mt[7])) * sl2;
+        // the reference maximum: the first block's, then moved (for the whole warp, whose O it
+        // rescales in tensor memory) when a row would produce weights above 2^8
+        float m_new = m_cur;
+        if (j == 0) {
+          m_new = mx;
+        } else if (__any_sync(0xffffffffu, mx > m_cur + kKtLazyLog2)) {
+          m_new = fmaxf(m_cur, mx);
+          const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m_cur - m_new);
+          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[b ^ 1], ((j - 1) >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[16];
+            tmem_ld_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * corr);
+            tmem_st_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+          }
+          l *= corr;
+        }
+        m_cur = m_new;
+        // a row that has seen nothing yet weighs nothing; one with an infinite score is undefined
+        const float neg = m_new == -INFINITY ? 0.f : m_new == INFINITY ? NAN : -m_new;
+        float rs[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1, p0, p1;
+            ffma2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]), sl2, neg, x0, x1);
+            if (((e >> 1) & 7) >= 5) {
+              exp2_poly2(x0, x1, p0, p1);
+              if (masked) {   // hidden keys must weigh exactly nothing
+                p0 = x0 == -INFINITY ? 0.f : p0;
+                p1 = x1 == -INFINITY ? 0.f : p1;
+              }
+            } else {
+              p0 = ex2_approx(x0);
+              p1 = ex2_approx(x1);
+            }
+            rs[0] += p0;
+            rs[1] += p1;
+            pk[e >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st_32x32b_x16(saddr + c * 16, pk);
+        }
+        l += rs[0] + rs[1];
+        tmem_st_wait();
+      }
+      // no warp is more than a block ahead of another here, and the producers reach block j + 4, the
+      // next to use this slot, only after P_j V_j, which waits for this arrival
+      if (threadIdx.x == 0) s_bad[(j + 4) & 7] = 0;
+      tc_fence_before();
+      mbar_arrive(&p_full[b]);
+    }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, &abort_flag));
+    if (ok && warp_live) {
+      tc_fence_after();
+      const long long item = (((long long)blockIdx.x * p.Hkv + h) * p.n_split + blockIdx.z) * KT_ROWS + row;
+      const float inv = p.n_split > 1 ? 1.f : l == 0.f ? 0.f : 1.0f / l;    // a row that sees nothing is zero
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t w[16];
+        if (n > 0) {
+          tmem_ld_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0;
+        }
+        float o[16];   // columns back in order
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[(e & 8) + ((e & 7) >> 1) + 4 * (e & 1)] = __uint_as_float(w[e]) * inv;
+        if (live && p.n_split == 1) {
+          __nv_bfloat16* out = p.O + qrow * p.ldo + col + 16 * c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                                            pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+        } else if (live) {
+          float* out = p.part + item * D + 16 * c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(out + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (live && p.n_split > 1) p.part_ml[item] = make_float2(m_cur, l);
+    }
+  } else {
+    // ---------------- producers ----------------
+    const int t = threadIdx.x - 128;
+    constexpr int G = D / KV4_GROUP;
+    const int P = 1 << p.P_log2;
+    const int rec = kv4_record_bytes(P, D), half = kv4_half_bytes(P, D), codes = kv4_codes_bytes(P, D);
+    const int32_t* table = p.table + (long long)a.r * p.max_blocks;
+    // unit u of this thread: groups 128 u .. of [K: key, group | V: key, group]; the key is the same
+    // for units an even distance apart
+    uint4 wd[C::UNITS];
+    uint32_t sc[C::UNITS];
+    uint32_t piece_bad = 0;
+    constexpr int KEYS_PER = 128 / G;       // keys that 128 neighbouring units cover (of keys or values)
+    auto page_of = [&](int j, int u) -> int {       // the page of unit u's key in block j; -1: past the keys
+      const int key = (b_lo + j) * KT_KEYS + (u * KEYS_PER + t / G) % KT_KEYS;
+      return j < n && key < a.len ? table[key >> p.P_log2] : -1;
+    };
+    auto load = [&](int j, const int (&page)[C::UNITS]) {
+      piece_bad = 0;
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) {
+        const int i = u * 128 + t, v = i >= KT_KEYS * G;
+        const int kin = (i / G) % KT_KEYS;
+        const int key = (b_lo + j) * KT_KEYS + kin;
+        wd[u] = make_uint4(0, 0, 0, 0);
+        sc[u] = 0;
+        if (j < n && key < a.len) {
+          if (page[u] >= 0 && page[u] < p.n_pages) {
+            const int o = key & (P - 1);
+            const uint8_t* at = p.cache + ((long long)page[u] * p.Hkv + h) * rec + v * half;
+            wd[u] = *reinterpret_cast<const uint4*>(at + o * (D / 2) + (i % G) * 16);
+            sc[u] = *(reinterpret_cast<const uint16_t*>(at + codes) + o * G + i % G);
+          } else {
+            piece_bad |= 1u << (kin >> 4);
+          }
+        }
+      }
+    };
+    int page[C::UNITS], next[C::UNITS];
+#pragma unroll
+    for (int u = 0; u < C::UNITS; ++u) page[u] = page_of(0, u);
+#pragma unroll
+    for (int u = 0; u < C::UNITS; ++u) next[u] = page_of(1, u);
+    if (n > 0) load(0, page);
+    // block j (loaded before) to its stage; the loads of block j + 1 are issued first
+    auto produce = [&](int j) -> bool {
+      const int st = j % C::STAGES;
+      uint4 cw[C::UNITS];
+      uint32_t cs[C::UNITS];
+      const uint32_t bad = piece_bad;
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) {
+        cw[u] = wd[u];
+        cs[u] = sc[u];
+        page[u] = next[u];
+      }
+      load(j + 1, page);
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) next[u] = page_of(j + 2, u);
+      if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag)))
+        return false;
+      uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) {
+        const int i = u * 128 + t, v = i >= KT_KEYS * G;
+        const int kin = (i / G) % KT_KEYS, g = i % G;
+        const uint32_t s2 = cs[u] | (cs[u] << 16), c2 = kv4_offset(s2);
+        const uint32_t w[4] = {cw[u].x, cw[u].y, cw[u].z, cw[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
+                                     kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
+          *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(kin, g * 4 + k, C::KV_PANEL)) = e;
+        }
+      }
+      if (bad != 0) {
+        atomicOr(&s_bad[j & 7], bad);
+        set_status(p.status, ROCS_ERR_INDEX);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&kv_full[st]);
+      return true;
+    };
+    const uint32_t qa = smem_u32(sQ), kva = smem_u32(sKV);
+    auto issue_s = [&](int j) -> bool {
+      const int st = j % C::STAGES;
+      if (!mbar_wait(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t ka = kva + st * 2 * C::KV_BYTES;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t qo = (ks >> 2) * C::Q_PANEL + (ks & 3) * 32, ko = (ks >> 2) * C::KV_PANEL + (ks & 3) * 32;
+        tc_mma_ss(tmem + C::S_COL + (j & 1) * KT_KEYS, sdesc(qa + qo, C::SBO, C::SW), sdesc(ka + ko, C::SBO, C::SW), IDESC_S,
+                  ks > 0 ? 1u : 0u);
+      }
+      tc_commit(&s_full[j & 1]);
+      return true;
+    };
+    auto issue_pv = [&](int j) -> bool {
+      const int st = j % C::STAGES;
+      if (!mbar_wait(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t va = kva + st * 2 * C::KV_BYTES + C::KV_BYTES;
+#pragma unroll
+      for (int pn = 0; pn < C::PANELS; ++pn)
+#pragma unroll
+        for (int ks = 0; ks < KT_KEYS / 16; ++ks)
+          tc_mma_ts(tmem + C::O_COL + pn * 64, tmem + C::S_COL + (j & 1) * KT_KEYS + ks * 8,
+                    sdesc(va + pn * C::KV_PANEL + ks * 16 * C::ROWB, C::SBO, C::SW), IDESC_O, (ks > 0 || j > 0) ? 1u : 0u);
+      tc_commit(&kv_empty[st]);
+      tc_commit(&pv_done[j & 1]);
+      return true;
+    };
+    if (warp != 4) {
+      for (int j = 0; j < n; ++j)
+        if (!produce(j)) break;
+    } else if (n > 0) {
+      // two blocks ahead of the P V being issued: while the softmax works on block j + 1, whose S is
+      // already in flight, this warp converts its share of block j + 2
+      bool ok = produce(0) && (n < 2 || produce(1));
+      if (lane == 0) ok = ok && mbar_wait(&q_full, 0, p.status, &abort_flag) && issue_s(0);
+      for (int j = 0; __shfl_sync(0xffffffffu, ok, 0) && j < n; ++j) {
+        if (lane == 0) ok = (j + 1 >= n || issue_s(j + 1)) && issue_pv(j);
+        __syncwarp();
+        if (j + 2 < n && !produce(j + 2)) break;
+      }
+      if (lane == 0) {
+        tc_commit(&drain);
+        mbar_wait(&drain, 0, p.status, nullptr);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long tiles, cudaStream_t s) {
+  using C = KtCfg<D>;
+  static bool attr[64] = {false};
+  if (ctx->device >= 64 || !attr[ctx->device]) {
+    rocs_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM),
+                                "cudaFuncSetAttribute(attn_kv4_tc)");
+    if (st != ROCS_OK) return st;
+    if (ctx->device < 64) attr[ctx->device] = true;
+  }
+  LaunchTimer lt_("attn_kv4_tc", s);
+  attn_kv4_tc_kernel<D><<<dim3((unsigned)tiles, p.Hkv, p.n_split), KT_THREADS, C::SMEM, s>>>(p);
+  return cuda_check(cudaGetLastError(), "attn_kv4_tc_kernel");
+}
+
+}  // namespace
+
+rocs_status launch_attn_kv4_tc(rocs_context* ctx, int d_h, const KaParams& p, long long tiles, cudaStream_t s) {
+  switch (d_h) {
+    case 32: return kt_launch<32>(ctx, p, tiles, s);
+    case 64: return kt_launch<64>(ctx, p, tiles, s);
+    default: return kt_launch<128>(ctx, p, tiles, s);
+  }
+}
+
+}  // namespace rocs
