@@ -84,6 +84,45 @@ __device__ __forceinline__ bool ka_tile(const KaParams& p, long long t, int T, K
   return true;
 }
 
+// The same for a whole block of 256 threads, in one round of loads up to 1024 requests (the start of a
+// tile is a chain of latencies: 3300 cycles with the warp's search, of some 20000 a tile): each
+// thread looks at up to four requests, and whoever finds the tile's publishes all there is to it.
+__device__ __forceinline__ bool ka_tile_block(const KaParams& p, long long t, int T, KaTile& a) {
+  __shared__ KaTile s_tile;
+  __shared__ int s_found;
+  if (p.B_R > 1024) return ka_tile(p, t, T, a);
+  if (threadIdx.x == 0) s_found = 0;
+  long long o[5];
+  int len[4];
+  const int r0 = threadIdx.x * 4;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) o[i] = r0 + i <= p.B_R ? p.offsets[r0 + i] : -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) len[i] = r0 + i < p.B_R ? p.kv_len[r0 + i] : -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i;
+    if (r >= p.B_R || o[i] < 0 || o[i + 1] < o[i] || o[i + 1] > p.rows || len[i] < 0 ||
+        len[i] > ((long long)p.max_blocks << p.P_log2))
+      continue;
+    const long long ti = t - (o[i] * p.share / T + r), n = (o[i + 1] - o[i]) * p.share;
+    if (ti < 0 || ti * T >= n) continue;
+    // with offsets in order no other request has this tile; otherwise any of them will do
+    if (atomicExch(&s_found, 1) == 0) {
+      s_tile.r = r;
+      s_tile.q0 = o[i];
+      s_tile.n_r = (int)(o[i + 1] - o[i]);
+      s_tile.n = (int)n;
+      s_tile.first = (int)(ti * T);
+      s_tile.len = len[i];
+    }
+  }
+  __syncthreads();
+  a = s_tile;
+  return s_found != 0;
+}
+
 // Keys that packed row m of the tile's request sees: [0, limit).
 __device__ __forceinline__ int ka_limit(const KaParams& p, const KaTile& a, int m) {
   return p.causal ? max(0, a.len - a.n_r + m / p.share + 1) : a.len;

@@ -2,19 +2,19 @@
 // 5th-generation tensor cores.
 //
 // One CTA takes 128 packed rows (query row x shared head) of one request against one key head, in
-// blocks of 64 keys; two CTAs share an SM, so that one's start and end hide behind the other.
+// blocks of 64 keys; three CTAs share an SM (two with d = 64 or 128), so that one's waits, start and end
+// hide behind the others.
 //   warps 0-3  softmax, one thread per row (TMEM lane): S is read from tensor memory, its maximum
-//              and exponentials are taken in registers (three pairs in eight on the FMA pipe), and P
+//              and exponentials are taken in registers, and P
 //              is written back over S as bf16 pairs, the A operand of P V.  The row's reference
 //              maximum moves only when a block exceeds it by more than 2^8.
-//   warps 4-7  producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
+//   warps 4-6  producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
 //              value at a time, a block ahead in registers, dequantises it (exactly) and writes it as
 //              bf16 into the operand's swizzled tile in shared memory.  The conversion is paid once
 //              per 128 rows; a copy of the codes through shared memory would only lengthen the way.
-//   warp 4     also issues the MMAs, between two blocks' conversions: S_j = Q K_j^T into one of two
-//              buffers, O += P_j V_j.  They execute in order, so S_{j+1} is in flight while the softmax
-//              works on S_j, and the P in a buffer is consumed before the S two blocks later lands on
-//              it.  (A warp of its own for them would cost every thread a fifth of its registers.)
+//   warp 7     issues the MMAs: S_j = Q K_j^T into one of two buffers, O += P_j V_j.  They execute in
+//              order, so S_{j+1} is there when the softmax is done with S_j, and the P in a buffer is
+//              consumed before the S two blocks later lands on it: one wait and one arrival a block.
 // Codes come out of a word as the pairs (0, 4), (1, 5), (2, 6), (3, 7); keys and queries keep that
 // order (a contraction index may be permuted), and the output's columns are put right as they are
 // stored.  Bound by the exponentials; all waits are bounded (ROCS_ERR_DEVICE_TIMEOUT), after which
@@ -32,7 +32,18 @@ namespace {
 constexpr int KT_ROWS = 128;
 constexpr int KT_KEYS = 64;
 constexpr int KT_THREADS = 256;
+constexpr int KT_PRODUCERS = 96;
 constexpr float kKtLazyLog2 = 8.0f;
+#ifndef KT_POLY
+#define KT_POLY 0
+#endif
+constexpr int kKtPoly = KT_POLY;
+#ifndef KT_PSLEEP
+#define KT_PSLEEP 200
+#endif
+#ifndef KT_MSLEEP
+#define KT_MSLEEP 32
+#endif
 
 template <int D>
 struct KtCfg {
@@ -43,11 +54,19 @@ struct KtCfg {
   static constexpr int Q_PANEL = KT_ROWS * ROWB, KV_PANEL = KT_KEYS * ROWB;
   static constexpr int Q_BYTES = PANELS * Q_PANEL, KV_BYTES = PANELS * KV_PANEL;   // of K, and of V
   static constexpr int STAGES = D == 32 ? 4 : D == 64 ? 3 : 2;
-  static constexpr int S_COL = 0, O_COL = 2 * KT_KEYS, TMEM_COLS = 256;
+  // tensor memory: two S buffers (64 columns each, P written over the first half as bf16 pairs) and O
+  // (D).  With d = 32 in two pieces, so that three CTAs fit the SM's 512 columns.
+  static constexpr int CTAS = D == 32 ? 3 : 2;
+  static constexpr int COLS = D == 32 ? 128 : 256, MORE_COLS = D == 32 ? 32 : 0;
+  // registers a thread after the split: the launch gives every thread LAUNCH
+  static constexpr int LAUNCH = CTAS == 3 ? 80 : 128, CONTROL = CTAS == 3 ? 56 : 128, SOFTMAX = CTAS == 3 ? 104 : 128;
+  static_assert(128 * (CONTROL + SOFTMAX) <= KT_THREADS * LAUNCH, "register split");
   static constexpr int USED = Q_BYTES + 2 * STAGES * KV_BYTES + 1024;
-  // two CTAs an SM, never three: a third could not have its tensor memory
-  static constexpr int SMEM = USED > 80 * 1024 ? USED : 80 * 1024;
-  static constexpr int UNITS = KT_KEYS * (D / KV4_GROUP) * 2 / 128;   // groups per producer thread and block
+  // no more CTAs an SM than tensor memory has room for
+  static constexpr int LEAST = 227 * 1024 / (CTAS + 1) / 1024 * 1024;
+  static constexpr int SMEM = USED > LEAST ? USED : LEAST;
+  static constexpr int ALL = KT_KEYS * (D / KV4_GROUP) * 2;             // groups of a block
+  static constexpr int UNITS = (ALL + KT_PRODUCERS - 1) / KT_PRODUCERS;   // ... per producer thread
 };
 
 // Byte offset of 16-byte unit c (of the whole row of D elements) of row r in a swizzled tile.
@@ -57,21 +76,39 @@ __device__ __forceinline__ uint32_t kt_unit(int r, int c, int panel_bytes) {
   return (uint32_t)((c >> 3) * panel_bytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// One arrival for the whole warp (32 arrivals at one barrier would queue up).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Eight elements of a row in the codes' order (0, 4, 1, 5, 2, 6, 3, 7).
 __device__ __forceinline__ uint4 kt_order(uint4 x) {
   return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
                     __byte_perm(x.y, x.w, 0x7632));
 }
 
+// (a, b) added to a pair of running sums, and the pair's sum.
+__device__ __forceinline__ void add2(uint64_t& s, float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s) : "l"(v));
+}
+__device__ __forceinline__ float sum2(uint64_t s) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(s));
+  return a + b;
+}
+
 template <int D>
-__global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaParams p) {
+__global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel(const KaParams p) {
   using C = KtCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(KT_ROWS, KT_KEYS, false);
   constexpr uint32_t IDESC_O = idesc_bf16(KT_ROWS, D == 128 ? 64 : D, true);
   extern __shared__ uint8_t kt_raw[];
   __shared__ uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], q_full, s_full[2], p_full[2], pv_done[2], drain;
   __shared__ uint32_t s_bad[8];            // per block (mod 8): 16-key pieces whose page does not exist
-  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t tmem_slot[2];
   __shared__ volatile int abort_flag;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kt_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
@@ -81,7 +118,7 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
 
   if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
   KaTile a;
-  if (!ka_tile(p, blockIdx.x, KT_ROWS, a)) return;
+  if (!ka_tile_block(p, blockIdx.x, KT_ROWS, a)) return;
   const int last = min(a.first + KT_ROWS, a.n) - 1;
   const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
   const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
@@ -92,30 +129,32 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
   if (threadIdx.x < 8) s_bad[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&kv_full[i], 128);
+      mbar_init(&kv_full[i], KT_PRODUCERS / 32);
       mbar_init(&kv_empty[i], 1);
     }
-    mbar_init(&q_full, 128);
+    mbar_init(&q_full, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 4) {
-    tmem_alloc(&tmem_slot, C::TMEM_COLS);
+  if (warp == 7) {
+    tmem_alloc(&tmem_slot[0], C::COLS);
+    if (C::MORE_COLS > 0) tmem_alloc(&tmem_slot[1], C::MORE_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t s_tmem = tmem_slot[0], o_tmem = C::MORE_COLS > 0 ? tmem_slot[1] : s_tmem + 2 * KT_KEYS;
 
   if (warp < 4) {
     // ---------------- softmax: thread = row = TMEM lane ----------------
+    if (C::CTAS == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX));
     const int row = threadIdx.x;
     const int m = a.first + row;
     const bool live = m < a.n;
@@ -131,9 +170,10 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
         *reinterpret_cast<uint4*>(sQ + kt_unit<D>(row, c, C::Q_PANEL)) = x;
       }
       fence_proxy_async_smem();
-      mbar_arrive(&q_full);
+      warp_arrive(&q_full);
     }
-    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t oaddr = o_tmem + lanes;
     const bool warp_live = a.first + warp * 32 < a.n;      // rows past the request's end are not computed
     const int limit = live ? ka_limit(p, a, m) : 0;
     const float sl2 = p.sl2;
@@ -143,14 +183,14 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
       const int b = j & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], (j >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
       tc_fence_after();
-      const uint32_t saddr = lane_addr + C::S_COL + b * KT_KEYS;
       if (warp_live) {
+        const uint32_t saddr = s_tmem + lanes + b * KT_KEYS;
         uint32_t v[2][32];
         tmem_ld_32x32b_x32(saddr, v[0]);
         tmem_ld_32x32b_x32(saddr + 32, v[1]);
+        const uint32_t bad = *(volatile uint32_t*)&s_bad[j & 7];
         tmem_ld_wait();
         const int k0 = (b_lo + j) * KT_KEYS;
-        const uint32_t bad = *(volatile uint32_t*)&s_bad[j & 7];
         const bool masked = bad != 0 || k0 + KT_KEYS > sees_all;
         if (masked) {
           const int valid = limit - k0;
@@ -180,18 +220,18 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint32_t w[16];
-            tmem_ld_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+            tmem_ld_32x32b_x16(oaddr + c * 16, w);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * corr);
-            tmem_st_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+            tmem_st_32x32b_x16(oaddr + c * 16, w);
           }
           l *= corr;
         }
         m_cur = m_new;
         // a row that has seen nothing yet weighs nothing; one with an infinite score is undefined
         const float neg = m_new == -INFINITY ? 0.f : m_new == INFINITY ? NAN : -m_new;
-        float rs[2] = {0.f, 0.f};
+        uint64_t rs = 0;   // two running sums
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
@@ -199,7 +239,7 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
           for (int e = 0; e < 32; e += 2) {
             float x0, x1, p0, p1;
             ffma2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]), sl2, neg, x0, x1);
-            if (((e >> 1) & 7) >= 5) {
+            if (((e >> 1) & 7) >= 8 - kKtPoly) {
               exp2_poly2(x0, x1, p0, p1);
               if (masked) {   // hidden keys must weigh exactly nothing
                 p0 = x0 == -INFINITY ? 0.f : p0;
@@ -209,20 +249,19 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
               p0 = ex2_approx(x0);
               p1 = ex2_approx(x1);
             }
-            rs[0] += p0;
-            rs[1] += p1;
+            add2(rs, p0, p1);
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
           tmem_st_32x32b_x16(saddr + c * 16, pk);
         }
-        l += rs[0] + rs[1];
+        l += sum2(rs);
         tmem_st_wait();
       }
-      // no warp is more than a block ahead of another here, and the producers reach block j + 4, the
+      // no softmax warp is more than a block ahead of another, and the producers reach block j + 4, the
       // next to use this slot, only after P_j V_j, which waits for this arrival
       if (threadIdx.x == 0) s_bad[(j + 4) & 7] = 0;
       tc_fence_before();
-      mbar_arrive(&p_full[b]);
+      warp_arrive(&p_full[b]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, &abort_flag));
     if (ok && warp_live) {
@@ -233,7 +272,7 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
       for (int c = 0; c < D / 16; ++c) {
         uint32_t w[16];
         if (n > 0) {
-          tmem_ld_32x32b_x16(lane_addr + C::O_COL + c * 16, w);
+          tmem_ld_32x32b_x16(oaddr + c * 16, w);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -256,145 +295,136 @@ __global__ void __launch_bounds__(KT_THREADS, 2) attn_kv4_tc_kernel(const KaPara
       }
       if (live && p.n_split > 1) p.part_ml[item] = make_float2(m_cur, l);
     }
-  } else {
+  } else if (warp < 7) {
     // ---------------- producers ----------------
+    if (C::CTAS == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
     const int t = threadIdx.x - 128;
     constexpr int G = D / KV4_GROUP;
     const int P = 1 << p.P_log2;
     const int rec = kv4_record_bytes(P, D), half = kv4_half_bytes(P, D), codes = kv4_codes_bytes(P, D);
     const int32_t* table = p.table + (long long)a.r * p.max_blocks;
-    // unit u of this thread: groups 128 u .. of [K: key, group | V: key, group]; the key is the same
-    // for units an even distance apart
+    // unit u of this thread: group i = u * 96 + t of [K: key, group | V: key, group]
     uint4 wd[C::UNITS];
     uint32_t sc[C::UNITS];
+    int next[C::UNITS];
     uint32_t piece_bad = 0;
-    constexpr int KEYS_PER = 128 / G;       // keys that 128 neighbouring units cover (of keys or values)
-    auto page_of = [&](int j, int u) -> int {       // the page of unit u's key in block j; -1: past the keys
-      const int key = (b_lo + j) * KT_KEYS + (u * KEYS_PER + t / G) % KT_KEYS;
-      return j < n && key < a.len ? table[key >> p.P_log2] : -1;
+    auto key_in = [&](int u) { return ((u * KT_PRODUCERS + t) / G) % KT_KEYS; };
+    auto has = [&](int u) { return C::ALL % KT_PRODUCERS == 0 || u * KT_PRODUCERS + t < C::ALL; };
+    auto pages = [&](int j) {                       // of block j's units; -1 where there is none
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) {
+        const int key = (b_lo + j) * KT_KEYS + key_in(u);
+        next[u] = j < n && key < a.len ? table[key >> p.P_log2] : -1;
+      }
     };
-    auto load = [&](int j, const int (&page)[C::UNITS]) {
+    auto load = [&](int j) {
       piece_bad = 0;
 #pragma unroll
       for (int u = 0; u < C::UNITS; ++u) {
-        const int i = u * 128 + t, v = i >= KT_KEYS * G;
-        const int kin = (i / G) % KT_KEYS;
-        const int key = (b_lo + j) * KT_KEYS + kin;
+        const int i = u * KT_PRODUCERS + t, v = i >= KT_KEYS * G;
+        const int key = (b_lo + j) * KT_KEYS + key_in(u);
         wd[u] = make_uint4(0, 0, 0, 0);
         sc[u] = 0;
-        if (j < n && key < a.len) {
-          if (page[u] >= 0 && page[u] < p.n_pages) {
+        if (has(u) && j < n && key < a.len) {
+          if (next[u] >= 0 && next[u] < p.n_pages) {
             const int o = key & (P - 1);
-            const uint8_t* at = p.cache + ((long long)page[u] * p.Hkv + h) * rec + v * half;
+            const uint8_t* at = p.cache + ((long long)next[u] * p.Hkv + h) * rec + v * half;
             wd[u] = *reinterpret_cast<const uint4*>(at + o * (D / 2) + (i % G) * 16);
             sc[u] = *(reinterpret_cast<const uint16_t*>(at + codes) + o * G + i % G);
           } else {
-            piece_bad |= 1u << (kin >> 4);
+            piece_bad |= 1u << (key_in(u) >> 4);
           }
         }
       }
     };
-    int page[C::UNITS], next[C::UNITS];
-#pragma unroll
-    for (int u = 0; u < C::UNITS; ++u) page[u] = page_of(0, u);
-#pragma unroll
-    for (int u = 0; u < C::UNITS; ++u) next[u] = page_of(1, u);
-    if (n > 0) load(0, page);
-    // block j (loaded before) to its stage; the loads of block j + 1 are issued first
-    auto produce = [&](int j) -> bool {
+    pages(0);
+    load(0);
+    pages(1);
+    for (int j = 0; j < n; ++j) {
       const int st = j % C::STAGES;
-      uint4 cw[C::UNITS];
-      uint32_t cs[C::UNITS];
-      const uint32_t bad = piece_bad;
-#pragma unroll
-      for (int u = 0; u < C::UNITS; ++u) {
-        cw[u] = wd[u];
-        cs[u] = sc[u];
-        page[u] = next[u];
-      }
-      load(j + 1, page);
-#pragma unroll
-      for (int u = 0; u < C::UNITS; ++u) next[u] = page_of(j + 2, u);
-      if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag)))
-        return false;
+      if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait_sleep(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag, KT_PSLEEP)))
+        break;
       uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
 #pragma unroll
       for (int u = 0; u < C::UNITS; ++u) {
-        const int i = u * 128 + t, v = i >= KT_KEYS * G;
-        const int kin = (i / G) % KT_KEYS, g = i % G;
-        const uint32_t s2 = cs[u] | (cs[u] << 16), c2 = kv4_offset(s2);
-        const uint32_t w[4] = {cw[u].x, cw[u].y, cw[u].z, cw[u].w};
+        const int i = u * KT_PRODUCERS + t, v = i >= KT_KEYS * G;
+        const int g = i % G;
+        const uint32_t s2 = sc[u] | (sc[u] << 16), c2 = kv4_offset(s2);
+        const uint32_t w[4] = {wd[u].x, wd[u].y, wd[u].z, wd[u].w};
+        if (has(u)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
-                                     kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
-          *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(kin, g * 4 + k, C::KV_PANEL)) = e;
+          for (int k = 0; k < 4; ++k) {
+            const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
+                                       kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
+            *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(key_in(u), g * 4 + k, C::KV_PANEL)) = e;
+          }
         }
       }
-      if (bad != 0) {
-        atomicOr(&s_bad[j & 7], bad);
+      if (piece_bad != 0) {
+        atomicOr(&s_bad[j & 7], piece_bad);
         set_status(p.status, ROCS_ERR_INDEX);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&kv_full[st]);
-      return true;
-    };
-    const uint32_t qa = smem_u32(sQ), kva = smem_u32(sKV);
+      warp_arrive(&kv_full[st]);
+      // the next block's loads after the proxy fence, which would wait for them too (157 instead of
+      // 227 us on 7601 causal rows)
+      load(j + 1);
+      pages(j + 2);
+    }
+  } else {
+    // ---------------- MMA issuer: the whole warp, so that its operands stay uniform ----------------
+    if (C::CTAS == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
+    const uint64_t qd = sdesc(smem_u32(sQ), C::SBO, C::SW), kd = sdesc(smem_u32(sKV), C::SBO, C::SW);
+    const bool one = elect_one();
     auto issue_s = [&](int j) -> bool {
       const int st = j % C::STAGES;
-      if (!mbar_wait(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag)) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag, KT_MSLEEP))) return false;
       tc_fence_after();
-      const uint32_t ka = kva + st * 2 * C::KV_BYTES;
+      if (one) {
+        const uint64_t k = kd + st * (2 * C::KV_BYTES >> 4);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t qo = (ks >> 2) * C::Q_PANEL + (ks & 3) * 32, ko = (ks >> 2) * C::KV_PANEL + (ks & 3) * 32;
-        tc_mma_ss(tmem + C::S_COL + (j & 1) * KT_KEYS, sdesc(qa + qo, C::SBO, C::SW), sdesc(ka + ko, C::SBO, C::SW), IDESC_S,
-                  ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma_ss(s_tmem + (j & 1) * KT_KEYS, qd + (((ks >> 2) * C::Q_PANEL + (ks & 3) * 32) >> 4),
+                    k + (((ks >> 2) * C::KV_PANEL + (ks & 3) * 32) >> 4), IDESC_S, ks > 0 ? 1u : 0u);
+        tc_commit(&s_full[j & 1]);
       }
-      tc_commit(&s_full[j & 1]);
       return true;
     };
     auto issue_pv = [&](int j) -> bool {
       const int st = j % C::STAGES;
-      if (!mbar_wait(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag)) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag, KT_MSLEEP))) return false;
       tc_fence_after();
-      const uint32_t va = kva + st * 2 * C::KV_BYTES + C::KV_BYTES;
+      if (one) {
+        const uint64_t v = kd + st * (2 * C::KV_BYTES >> 4) + (C::KV_BYTES >> 4);
+        const uint32_t acc = j > 0 ? 1u : 0u;
 #pragma unroll
-      for (int pn = 0; pn < C::PANELS; ++pn)
+        for (int pn = 0; pn < C::PANELS; ++pn)
 #pragma unroll
-        for (int ks = 0; ks < KT_KEYS / 16; ++ks)
-          tc_mma_ts(tmem + C::O_COL + pn * 64, tmem + C::S_COL + (j & 1) * KT_KEYS + ks * 8,
-                    sdesc(va + pn * C::KV_PANEL + ks * 16 * C::ROWB, C::SBO, C::SW), IDESC_O, (ks > 0 || j > 0) ? 1u : 0u);
-      tc_commit(&kv_empty[st]);
-      tc_commit(&pv_done[j & 1]);
+          for (int ks = 0; ks < KT_KEYS / 16; ++ks)
+            tc_mma_ts(o_tmem + pn * 64, s_tmem + (j & 1) * KT_KEYS + ks * 8,
+                      v + ((pn * C::KV_PANEL + ks * 16 * C::ROWB) >> 4), IDESC_O, ks > 0 ? 1u : acc);
+        tc_commit(&kv_empty[st]);
+        tc_commit(&pv_done[j & 1]);
+      }
       return true;
     };
-    if (warp != 4) {
-      for (int j = 0; j < n; ++j)
-        if (!produce(j)) break;
-    } else if (n > 0) {
-      // two blocks ahead of the P V being issued: while the softmax works on block j + 1, whose S is
-      // already in flight, this warp converts its share of block j + 2
-      bool ok = produce(0) && (n < 2 || produce(1));
-      if (lane == 0) ok = ok && mbar_wait(&q_full, 0, p.status, &abort_flag) && issue_s(0);
-      for (int j = 0; __shfl_sync(0xffffffffu, ok, 0) && j < n; ++j) {
-        if (lane == 0) ok = (j + 1 >= n || issue_s(j + 1)) && issue_pv(j);
-        __syncwarp();
-        if (j + 2 < n && !produce(j + 2)) break;
-      }
-      if (lane == 0) {
-        tc_commit(&drain);
-        mbar_wait(&drain, 0, p.status, nullptr);
-      }
-      __syncwarp();
+    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(&q_full, 0, p.status, &abort_flag, KT_MSLEEP));
+    if (ok && n > 0) ok = issue_s(0) && (n < 2 || issue_s(1));
+    for (int j = 0; ok && j < n; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
+    __syncwarp();
+    if (one) {
+      tc_commit(&drain);
+      mbar_wait(&drain, 0, p.status, nullptr);
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 7) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(s_tmem, C::COLS);
+    if (C::MORE_COLS > 0) tmem_dealloc(o_tmem, C::MORE_COLS);
   }
 }
 
@@ -406,6 +436,15 @@ rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long tiles, cud
     rocs_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM),
                                 "cudaFuncSetAttribute(attn_kv4_tc)");
     if (st != ROCS_OK) return st;
+    // the softmax warps raise their register limit out of the launch's allocation; refuse to launch if
+    // the compiled kernel was given fewer registers than that split needs
+    cudaFuncAttributes fa;
+    st = cuda_check(cudaFuncGetAttributes(&fa, attn_kv4_tc_kernel<D>), "cudaFuncGetAttributes(attn_kv4_tc)");
+    if (st != ROCS_OK) return st;
+    if (C::CTAS == 3 && fa.numRegs < C::LAUNCH) {
+      set_error("attn_kv4_tc: kernel compiled with %d registers per thread, below the warpgroup split", fa.numRegs);
+      return ROCS_ERR_UNSUPPORTED;
+    }
     if (ctx->device < 64) attr[ctx->device] = true;
   }
   LaunchTimer lt_("attn_kv4_tc", s);
