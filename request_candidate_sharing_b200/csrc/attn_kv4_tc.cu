@@ -8,7 +8,7 @@
 //              and exponentials are taken in registers, and P
 //              is written back over S as bf16 pairs, the A operand of P V.  The row's reference
 //              maximum moves only when a block exceeds it by more than 2^8.
-//   warps 4-6  producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
+//   warps 4-6  (and 8-10 with d = 64 or 128) producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
 //              value at a time, a block ahead in registers, dequantises it (exactly) and writes it as
 //              bf16 into the operand's swizzled tile in shared memory.  The conversion is paid once
 //              per 128 rows; a copy of the codes through shared memory would only lengthen the way.
@@ -31,19 +31,9 @@ namespace {
 
 constexpr int KT_ROWS = 128;
 constexpr int KT_KEYS = 64;
-constexpr int KT_THREADS = 256;
-constexpr int KT_PRODUCERS = 96;
 constexpr float kKtLazyLog2 = 8.0f;
-#ifndef KT_POLY
-#define KT_POLY 0
-#endif
-constexpr int kKtPoly = KT_POLY;
-#ifndef KT_PSLEEP
-#define KT_PSLEEP 200
-#endif
-#ifndef KT_MSLEEP
-#define KT_MSLEEP 32
-#endif
+// pauses between polls of the roles off the critical path, whose polls take issue slots from the softmax
+constexpr unsigned kKtProducerSleepNs = 200, kKtIssuerSleepNs = 32;
 
 template <int D>
 struct KtCfg {
@@ -58,15 +48,18 @@ struct KtCfg {
   // (D).  With d = 32 in two pieces, so that three CTAs fit the SM's 512 columns.
   static constexpr int CTAS = D == 32 ? 3 : 2;
   static constexpr int COLS = D == 32 ? 128 : 256, MORE_COLS = D == 32 ? 32 : 0;
+  // three producer warps (of a warpgroup with the MMA issuer), or six: with d = 64, three took longer
+  // over a block than the softmax does
+  static constexpr int TEAMS = D == 32 ? 1 : 2, THREADS = 128 + 128 * TEAMS, PRODUCERS = 96 * TEAMS;
   // registers a thread after the split: the launch gives every thread LAUNCH
-  static constexpr int LAUNCH = CTAS == 3 ? 80 : 128, CONTROL = CTAS == 3 ? 56 : 128, SOFTMAX = CTAS == 3 ? 104 : 128;
-  static_assert(128 * (CONTROL + SOFTMAX) <= KT_THREADS * LAUNCH, "register split");
+  static constexpr int LAUNCH = 80, CONTROL = 56, SOFTMAX = D == 32 ? 104 : 128;
+  static_assert(128 * (TEAMS * CONTROL + SOFTMAX) <= THREADS * LAUNCH, "register split");
   static constexpr int USED = Q_BYTES + 2 * STAGES * KV_BYTES + 1024;
   // no more CTAs an SM than tensor memory has room for
   static constexpr int LEAST = 227 * 1024 / (CTAS + 1) / 1024 * 1024;
   static constexpr int SMEM = USED > LEAST ? USED : LEAST;
   static constexpr int ALL = KT_KEYS * (D / KV4_GROUP) * 2;             // groups of a block
-  static constexpr int UNITS = (ALL + KT_PRODUCERS - 1) / KT_PRODUCERS;   // ... per producer thread
+  static constexpr int UNITS = (ALL + PRODUCERS - 1) / PRODUCERS;   // ... per producer thread
 };
 
 // Byte offset of 16-byte unit c (of the whole row of D elements) of row r in a swizzled tile.
@@ -101,7 +94,7 @@ __device__ __forceinline__ float sum2(uint64_t s) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel(const KaParams p) {
+__global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel(const KaParams p) {
   using C = KtCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(KT_ROWS, KT_KEYS, false);
   constexpr uint32_t IDESC_O = idesc_bf16(KT_ROWS, D == 128 ? 64 : D, true);
@@ -113,7 +106,7 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kt_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
   uint8_t* sKV = base + C::Q_BYTES;        // [STAGES][K | V]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int h = blockIdx.y;
 
   if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
@@ -129,7 +122,7 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
   if (threadIdx.x < 8) s_bad[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&kv_full[i], KT_PRODUCERS / 32);
+      mbar_init(&kv_full[i], C::PRODUCERS / 32);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(&q_full, 4);
@@ -154,7 +147,7 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
 
   if (warp < 4) {
     // ---------------- softmax: thread = row = TMEM lane ----------------
-    if (C::CTAS == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX));
     const int row = threadIdx.x;
     const int m = a.first + row;
     const bool live = m < a.n;
@@ -239,16 +232,8 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
           for (int e = 0; e < 32; e += 2) {
             float x0, x1, p0, p1;
             ffma2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]), sl2, neg, x0, x1);
-            if (((e >> 1) & 7) >= 8 - kKtPoly) {
-              exp2_poly2(x0, x1, p0, p1);
-              if (masked) {   // hidden keys must weigh exactly nothing
-                p0 = x0 == -INFINITY ? 0.f : p0;
-                p1 = x1 == -INFINITY ? 0.f : p1;
-              }
-            } else {
-              p0 = ex2_approx(x0);
-              p1 = ex2_approx(x1);
-            }
+            p0 = ex2_approx(x0);
+            p1 = ex2_approx(x1);
             add2(rs, p0, p1);
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
@@ -295,90 +280,98 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
       }
       if (live && p.n_split > 1) p.part_ml[item] = make_float2(m_cur, l);
     }
-  } else if (warp < 7) {
+  } else if (warp != 7) {
     // ---------------- producers ----------------
-    if (C::CTAS == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
-    const int t = threadIdx.x - 128;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
+    const int t = threadIdx.x - (warp < 8 ? 128 : 160);     // (warp 11 has nothing to do)
     constexpr int G = D / KV4_GROUP;
     const int P = 1 << p.P_log2;
-    const int rec = kv4_record_bytes(P, D), half = kv4_half_bytes(P, D), codes = kv4_codes_bytes(P, D);
     const int32_t* table = p.table + (long long)a.r * p.max_blocks;
-    // unit u of this thread: group i = u * 96 + t of [K: key, group | V: key, group]
+    // unit u of this thread: group i = u * PRODUCERS + t of [K: key, group | V: key, group].  A block starts on
+    // a page's or (128 tokens) half page's edge, so a unit's place in its record stays the same.
     uint4 wd[C::UNITS];
     uint32_t sc[C::UNITS];
-    int next[C::UNITS];
+    int next[C::UNITS], key_in[C::UNITS];
+    uint32_t code_at[C::UNITS], scale_at[C::UNITS];
     uint32_t piece_bad = 0;
-    auto key_in = [&](int u) { return ((u * KT_PRODUCERS + t) / G) % KT_KEYS; };
-    auto has = [&](int u) { return C::ALL % KT_PRODUCERS == 0 || u * KT_PRODUCERS + t < C::ALL; };
-    auto pages = [&](int j) {                       // of block j's units; -1 where there is none
 #pragma unroll
-      for (int u = 0; u < C::UNITS; ++u) {
-        const int key = (b_lo + j) * KT_KEYS + key_in(u);
-        next[u] = j < n && key < a.len ? table[key >> p.P_log2] : -1;
-      }
+    for (int u = 0; u < C::UNITS; ++u) {
+      const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
+      const bool has = i < C::ALL;
+      key_in[u] = has ? (i / G) % KT_KEYS : 1 << 30;       // a unit too many lies past every key
+      const int o = key_in[u] & (P - 1);
+      code_at[u] = v * kv4_half_bytes(P, D) + o * (D / 2) + (i % G) * 16;
+      scale_at[u] = v * kv4_half_bytes(P, D) + kv4_codes_bytes(P, D) + (o * G + i % G) * 2;
+    }
+    auto pages = [&](int j) {                       // of block j's units; -1 where there is none
+      const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
+      const int32_t* at = table + (((long long)(b_lo + j) * KT_KEYS) >> p.P_log2);
+#pragma unroll
+      for (int u = 0; u < C::UNITS; ++u) next[u] = key_in[u] < left ? at[key_in[u] >> p.P_log2] : -1;
     };
     auto load = [&](int j) {
       piece_bad = 0;
+      const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
+      const int odd = P > KT_KEYS ? (b_lo + j) & 1 : 0;
+      const uint8_t* head = p.cache + (long long)h * kv4_record_bytes(P, D);
+      const long long stride = (long long)p.Hkv * kv4_record_bytes(P, D);
 #pragma unroll
       for (int u = 0; u < C::UNITS; ++u) {
-        const int i = u * KT_PRODUCERS + t, v = i >= KT_KEYS * G;
-        const int key = (b_lo + j) * KT_KEYS + key_in(u);
         wd[u] = make_uint4(0, 0, 0, 0);
         sc[u] = 0;
-        if (has(u) && j < n && key < a.len) {
+        if (key_in[u] < left) {
           if (next[u] >= 0 && next[u] < p.n_pages) {
-            const int o = key & (P - 1);
-            const uint8_t* at = p.cache + ((long long)next[u] * p.Hkv + h) * rec + v * half;
-            wd[u] = *reinterpret_cast<const uint4*>(at + o * (D / 2) + (i % G) * 16);
-            sc[u] = *(reinterpret_cast<const uint16_t*>(at + codes) + o * G + i % G);
+            const uint8_t* at = head + next[u] * stride;
+            wd[u] = *reinterpret_cast<const uint4*>(at + code_at[u] + odd * kv4_codes_bytes(KT_KEYS, D));
+            sc[u] = *reinterpret_cast<const uint16_t*>(at + scale_at[u] + odd * kv4_scales_bytes(KT_KEYS, D));
           } else {
-            piece_bad |= 1u << (key_in(u) >> 4);
+            piece_bad |= 1u << (key_in[u] >> 4);
           }
         }
       }
     };
-    pages(0);
-    load(0);
-    pages(1);
-    for (int j = 0; j < n; ++j) {
-      const int st = j % C::STAGES;
-      if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait_sleep(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag, KT_PSLEEP)))
-        break;
-      uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
+    if (t < C::PRODUCERS) {
+      pages(0);
+      load(0);
+      pages(1);
+      for (int j = 0; j < n; ++j) {
+        const int st = j % C::STAGES;
+        if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait_sleep(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag, kKtProducerSleepNs)))
+          break;
+        uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
 #pragma unroll
-      for (int u = 0; u < C::UNITS; ++u) {
-        const int i = u * KT_PRODUCERS + t, v = i >= KT_KEYS * G;
-        const int g = i % G;
-        const uint32_t s2 = sc[u] | (sc[u] << 16), c2 = kv4_offset(s2);
-        const uint32_t w[4] = {wd[u].x, wd[u].y, wd[u].z, wd[u].w};
-        if (has(u)) {
+        for (int u = 0; u < C::UNITS; ++u) {
+          const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
+          const int g = i % G;
+          const uint32_t s2 = sc[u] | (sc[u] << 16), c2 = kv4_offset(s2);
+          const uint32_t w[4] = {wd[u].x, wd[u].y, wd[u].z, wd[u].w};
+          if (key_in[u] < KT_KEYS) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
-                                       kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
-            *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(key_in(u), g * 4 + k, C::KV_PANEL)) = e;
+            for (int k = 0; k < 4; ++k) {
+              const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
+                                         kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
+              *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(key_in[u], g * 4 + k, C::KV_PANEL)) = e;
+            }
           }
         }
+        if (piece_bad != 0) {
+          atomicOr(&s_bad[j & 7], piece_bad);
+          set_status(p.status, ROCS_ERR_INDEX);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&kv_full[st]);
+        load(j + 1);
+        pages(j + 2);
       }
-      if (piece_bad != 0) {
-        atomicOr(&s_bad[j & 7], piece_bad);
-        set_status(p.status, ROCS_ERR_INDEX);
-      }
-      fence_proxy_async_smem();
-      warp_arrive(&kv_full[st]);
-      // the next block's loads after the proxy fence, which would wait for them too (157 instead of
-      // 227 us on 7601 causal rows)
-      load(j + 1);
-      pages(j + 2);
     }
   } else {
     // ---------------- MMA issuer: the whole warp, so that its operands stay uniform ----------------
-    if (C::CTAS == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
     const uint64_t qd = sdesc(smem_u32(sQ), C::SBO, C::SW), kd = sdesc(smem_u32(sKV), C::SBO, C::SW);
     const bool one = elect_one();
     auto issue_s = [&](int j) -> bool {
       const int st = j % C::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag, KT_MSLEEP))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
       tc_fence_after();
       if (one) {
         const uint64_t k = kd + st * (2 * C::KV_BYTES >> 4);
@@ -392,7 +385,7 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
     };
     auto issue_pv = [&](int j) -> bool {
       const int st = j % C::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag, KT_MSLEEP))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
       tc_fence_after();
       if (one) {
         const uint64_t v = kd + st * (2 * C::KV_BYTES >> 4) + (C::KV_BYTES >> 4);
@@ -408,7 +401,7 @@ __global__ void __launch_bounds__(KT_THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel
       }
       return true;
     };
-    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(&q_full, 0, p.status, &abort_flag, KT_MSLEEP));
+    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(&q_full, 0, p.status, &abort_flag, kKtIssuerSleepNs));
     if (ok && n > 0) ok = issue_s(0) && (n < 2 || issue_s(1));
     for (int j = 0; ok && j < n; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
     __syncwarp();
@@ -441,14 +434,14 @@ rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long tiles, cud
     cudaFuncAttributes fa;
     st = cuda_check(cudaFuncGetAttributes(&fa, attn_kv4_tc_kernel<D>), "cudaFuncGetAttributes(attn_kv4_tc)");
     if (st != ROCS_OK) return st;
-    if (C::CTAS == 3 && fa.numRegs < C::LAUNCH) {
+    if (fa.numRegs < C::LAUNCH) {
       set_error("attn_kv4_tc: kernel compiled with %d registers per thread, below the warpgroup split", fa.numRegs);
       return ROCS_ERR_UNSUPPORTED;
     }
     if (ctx->device < 64) attr[ctx->device] = true;
   }
   LaunchTimer lt_("attn_kv4_tc", s);
-  attn_kv4_tc_kernel<D><<<dim3((unsigned)tiles, p.Hkv, p.n_split), KT_THREADS, C::SMEM, s>>>(p);
+  attn_kv4_tc_kernel<D><<<dim3((unsigned)tiles, p.Hkv, p.n_split), C::THREADS, C::SMEM, s>>>(p);
   return cuda_check(cudaGetLastError(), "attn_kv4_tc_kernel");
 }
 
