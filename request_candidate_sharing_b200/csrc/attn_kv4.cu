@@ -31,6 +31,12 @@
 namespace rocs {
 namespace {
 
+#ifndef KA_WANT
+#define KA_WANT 4LL
+#endif
+#ifndef KT_WANT
+#define KT_WANT 4LL
+#endif
 constexpr int KA_WARPS = 4;
 constexpr int kTcRows = 32;     // packed rows a request above which the 128-row tensor-core tiles pay
 constexpr int KA_CHUNK = 64;    // keys per stage of a warp's ring
@@ -380,32 +386,82 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   }
 }
 
-// Joins the splits of each (tile, head), in order.
+// Joins the splits of each (tile, head), in a fixed order.  D / 2 threads take a row (a pair of
+// columns each); the block's 256 / D groups of them take a row each where splits are few, else they
+// share one row's splits among them, with four splits' loads in flight a thread.
+constexpr int KJ_SPLITS = 8;      // splits above which the groups share a row
 template <int D, int T>
-__global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p) {
+__global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, int rows_per_block) {
+  constexpr int GROUPS = 256 / D;
+  __shared__ float s_part[GROUPS][D + 2];
   KaTile a;
   if (!ka_tile(p, blockIdx.x, T, a)) return;
-  const int h = blockIdx.y;
+  const int h = blockIdx.y, grp = threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
+  const bool shared_row = p.n_split > KJ_SPLITS;
+  const int row_step = shared_row ? 1 : GROUPS, split_step = shared_row ? GROUPS : 1;
   const long long item0 = ((long long)blockIdx.x * p.Hkv + h) * p.n_split;
-  for (int i = threadIdx.x; i < T * (D / 2); i += 128) {
-    const int row = i / (D / 2), d = 2 * (i % (D / 2));
-    const int m = a.first + row;
-    if (m >= a.n) break;
-    float top = -INFINITY;
-    for (int s = 0; s < p.n_split; ++s) top = fmaxf(top, p.part_ml[(item0 + s) * T + row].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, x = 0.f, y = 0.f;
-    for (int s = 0; s < p.n_split; ++s) {
-      const float2 ml = p.part_ml[(item0 + s) * T + row];
-      const float2 v = *reinterpret_cast<const float2*>(p.part + ((item0 + s) * T + row) * D + d);
-      const float f = ex2_approx(ml.x - ref);
-      l = fmaf(f, ml.y, l);
-      x = fmaf(f, v.x, x);
-      y = fmaf(f, v.y, y);
+  const int row_end = min((int)(blockIdx.z + 1) * rows_per_block, a.n - a.first);
+  for (int row0 = blockIdx.z * rows_per_block; row0 < row_end; row0 += row_step) {
+    const int row = row0 + (shared_row ? 0 : grp);
+    float top = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+    if (row < row_end) {
+      for (int s0 = shared_row ? grp : 0; s0 < p.n_split; s0 += 4 * split_step) {
+        float2 ml[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int sp = s0 + i * split_step;
+          ml[i] = make_float2(-INFINITY, 0.f);
+          v[i] = make_float2(0.f, 0.f);
+          if (sp < p.n_split) {
+            ml[i] = p.part_ml[(item0 + sp) * T + row];
+            v[i] = *reinterpret_cast<const float2*>(p.part + ((item0 + sp) * T + row) * D + d);
+          }
+        }
+        float m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[i].x);
+        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx(top - ref);
+        l *= f; x *= f; y *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = ex2_approx(ml[i].x - ref);
+          l = fmaf(e, ml[i].y, l);
+          x = fmaf(e, v[i].x, x);
+          y = fmaf(e, v[i].y, y);
+        }
+        top = m;
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
+    if (shared_row) {
+      s_part[grp][d] = x;
+      s_part[grp][d + 1] = y;
+      if (d == 0) {
+        s_part[grp][D] = top;
+        s_part[grp][D + 1] = l;
+      }
+      __syncthreads();
+      if (grp == 0) {
+        float m = top;
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) m = fmaxf(m, s_part[g][D]);
+        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx(top - ref);
+        l *= f; x *= f; y *= f;
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) {
+          const float e = ex2_approx(s_part[g][D] - ref);
+          l = fmaf(e, s_part[g][D + 1], l);
+          x = fmaf(e, s_part[g][d], x);
+          y = fmaf(e, s_part[g][d + 1], y);
+        }
+      }
+      __syncthreads();
+    }
+    if (row < row_end && (!shared_row || grp == 0)) {
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const int m = a.first + row;
+      __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
+      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
+    }
   }
 }
 
@@ -428,7 +484,7 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   // fill about twice the resident blocks (four an SM); a split has at least four chunks a warp
   const long long busy = (packed + k.T - 1) / k.T;
   const long long items = (busy < 1 ? 1 : busy) * d.H_kv;
-  const long long want = (k.NT > 0 ? 8LL : 4LL) * ctx->num_sms;
+  const long long want = (k.NT > 0 ? KA_WANT : KT_WANT) * ctx->num_sms;
   const long long longest = ((long long)max_blocks * d.page_size + KA_CHUNK - 1) / KA_CHUNK;
   long long split = items >= want / 2 ? 1 : want / items;
   const long long most = longest / (k.NT > 0 ? 4 * KA_WARPS : 8);
@@ -445,7 +501,9 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
 template <int D, int T>
 rocs_status ka_join(const KaParams& p, const KaPlan& k, cudaStream_t s) {
   LaunchTimer lt_("attn_kv4_join", s);
-  attn_kv4_join_kernel<D, T><<<dim3((unsigned)k.tiles, p.Hkv), 128, 0, s>>>(p);
+  // a block takes one row of many splits, or 16 rows of a few
+  const int rows = k.n_split > KJ_SPLITS ? 1 : T < 16 ? T : 16;
+  attn_kv4_join_kernel<D, T><<<dim3((unsigned)k.tiles, p.Hkv, T / rows), 128, 0, s>>>(p, rows);
   return cuda_check(cudaGetLastError(), "attn_kv4_join_kernel");
 }
 
