@@ -11,40 +11,42 @@
 //   S^T: a lane takes whole words of a key's row (d / 32 neighbouring ones), whose nibbles (0, 4),
 //        (1, 5), (2, 6), (3, 7) are the bf16 pairs; the queries are loaded in that order once;
 //   O^T: a lane takes the word of its eight output elements from four keys, and pairs equal nibbles
-//        of two keys; rows rho = 0..7 of a score tile are the keys (rho >> 1) + 4 (rho & 1), so that
-//        the words of the lanes' first keys lie side by side (no bank conflicts up to d = 64).
+//        of two keys (ka_key says which rows of a score tile are which keys).
 // P^T moves from the accumulator's layout to the operand's by an 8x8 transpose in registers.
 //
 // Bound by the cache's bytes.  A block of four warps has the keys of one (tile, head, split); each
 // warp streams its own 64-key chunks through a ring of bulk copies and keeps its own running
 // maximum, sum and output, joined through shared memory at the end, so the loop has no block-wide
-// wait.  Where the (tile, head) items are too few to fill the GPU the keys are split over blocks,
+// wait.  Short histories of many requests give each warp a head of its own instead.  Where the (tile, head) items are too few to fill the GPU the keys are split over blocks,
 // whose partial results a second launch joins in a fixed order.
 #include <float.h>
+
+#include <type_traits>
 
 #include "attn_kv4.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "mma_frag.cuh"
+#include "tc_attn.cuh"
 
 namespace rocs {
 namespace {
 
-#ifndef KA_WANT
-#define KA_WANT 4LL
-#endif
-#ifndef KT_WANT
-#define KT_WANT 4LL
+#ifndef KA_FULL
+#define KA_FULL 16LL
 #endif
 constexpr int KA_WARPS = 4;
 constexpr int kTcRows = 32;     // packed rows a request above which the 128-row tensor-core tiles pay
-constexpr int KA_CHUNK = 64;    // keys per stage of a warp's ring
+constexpr int KA_CHUNK = 64;    // keys scored at a time
+constexpr float kKaLazyLog2 = 8.0f;   // a row's reference maximum moves when a chunk exceeds it by this much
 
 template <int D>
 struct KaCfg {
-  static constexpr int STAGE = KA_CHUNK * D * 9 / 8;
-  static constexpr int STAGES = D == 32 ? 4 : D == 64 ? 3 : 2;
+  static constexpr int KEYS = D == 32 ? 128 : 64;          // keys per stage of a warp's ring
+  static constexpr int KEYS_LOG2 = D == 32 ? 7 : 6;
+  static constexpr int STAGE = KEYS * D * 9 / 8;
+  static constexpr int STAGES = D == 128 ? 2 : 3;
   static constexpr int RING = STAGE * STAGES;
   static constexpr int SMEM = KA_WARPS * RING;
 };
@@ -68,7 +70,18 @@ __device__ __forceinline__ void ka_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-template <int D, int NT>
+// The key, of 16 neighbouring ones, that row rho of a score tile stands for.  d = 32: 0, 2, 4, .. and 1, 3,
+// 5, .., which gives a lane pairs and fours of neighbouring keys, whose scales are one load.  Wider heads:
+// in each half 0, 4, 1, 5, 2, 6, 3, 7, so that the words that the lanes read of their values lie in
+// different banks.
+template <int D>
+__device__ __forceinline__ int ka_key(int rho) {
+  if constexpr (D == 32) return 2 * (rho & 7) + (rho >> 3);
+  return (rho & 8) + ((rho & 7) >> 1) + 4 * (rho & 1);
+}
+
+// BIG: pages of at least 64 tokens, so that a chunk lies in one page's record.
+template <int D, int NT, bool BIG>
 __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams p) {
   using C = KaCfg<D>;
   constexpr int T = 8 * NT;
@@ -80,7 +93,9 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   __shared__ uint64_t bars[KA_WARPS][C::STAGES];
   __shared__ float s_m[KA_WARPS][T], s_l[KA_WARPS][T];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3;
-  const int h = blockIdx.y;
+  // p.per_item warps (1, 2 or 4) share a (tile, head); the block has 4 / per_item neighbouring heads
+  const int heads = KA_WARPS / p.per_item, part = warp & (p.per_item - 1);
+  const int h = blockIdx.y * heads + warp / p.per_item;
 
   if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
   KaTile a;
@@ -88,7 +103,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   const int last = min(a.first + T, a.n) - 1;       // last packed row of the tile
   const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
   const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
-  const int chunks = (seen + KA_CHUNK - 1) / KA_CHUNK;
+  const int chunks = h < p.Hkv ? (seen + C::KEYS - 1) / C::KEYS : 0;
   const int c_lo = (int)((long long)chunks * blockIdx.z / p.n_split);
   const int c_hi = (int)((long long)chunks * (blockIdx.z + 1) / p.n_split);
 
@@ -99,39 +114,40 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   fence_proxy_async_smem();
   __syncwarp();
 
-  // a chunk's pages: pieces of PE = min(page, 64) keys, each a record of PE keys in the stage
-  const int PE_log2 = min(p.P_log2, 6), PE = 1 << PE_log2;
-  const int pieces = KA_CHUNK >> PE_log2;
+  // a stage's pages: pieces of PE = min(page, KEYS) keys, each a record of PE keys in the stage
+  const int PE_log2 = min(p.P_log2, C::KEYS_LOG2), PE = 1 << PE_log2;
+  const int pieces = C::KEYS >> PE_log2;
   const int rec = kv4_record_bytes(PE, D);
   const int32_t* table = p.table + (long long)a.r * p.max_blocks;
-  auto page_of = [&](int c) -> int {      // lane i < pieces: the page of piece i of chunk c (-2: none is needed)
-    const long long key = (long long)c * KA_CHUNK + ((long long)lane << PE_log2);
+  const uint8_t* head = p.cache + (long long)h * kv4_record_bytes(1 << p.P_log2, D);
+  const long long page_bytes = (long long)p.Hkv * kv4_record_bytes(1 << p.P_log2, D);
+  auto page_of = [&](int c) -> int {      // lane i < pieces: the page of piece i of stage c (-2: none is needed)
+    const long long key = (long long)c * C::KEYS + ((long long)lane << PE_log2);
     return lane < pieces && c < c_hi && key < a.len ? table[key >> p.P_log2] : -2;
   };
-  uint32_t bad_of = 0;                    // 4 bits per stage: pieces whose page does not exist
+  uint32_t bad_of = 0;                    // 8 bits per stage: pieces whose page does not exist
   auto issue = [&](int c, int st, int page) {
     const bool ok = page >= 0 && page < p.n_pages;
     const uint32_t mask = __ballot_sync(0xffffffffu, ok);
     const uint32_t bad = __ballot_sync(0xffffffffu, !ok && page != -2);
-    bad_of = (bad_of & ~(15u << (4 * st))) | ((bad & 15u) << (4 * st));
+    bad_of = (bad_of & ~(255u << (8 * st))) | (bad << (8 * st));
     if (bad != 0 && lane == 0) set_status(p.status, ROCS_ERR_INDEX);
     uint64_t* bar = &bars[warp][st];
     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mask) * rec));
     __syncwarp();
     if (ok) {
       uint8_t* dst = ring + st * C::STAGE + lane * rec;
-      const long long P = 1LL << p.P_log2;
-      const uint8_t* src = p.cache + ((long long)page * p.Hkv + h) * kv4_record_bytes((int)P, D);
-      if (p.P_log2 <= 6) {
+      const uint8_t* src = head + page * page_bytes;
+      if (p.P_log2 <= C::KEYS_LOG2) {
         bulk_load(dst, src, rec, bar);
       } else {                            // half of a 128-token page: its four parts one by one
-        const int o = (c & 1) * KA_CHUNK;
-        constexpr int CB = kv4_codes_bytes(KA_CHUNK, D), SB = kv4_scales_bytes(KA_CHUNK, D);
+        const int P = 1 << p.P_log2, o = (c & 1) * C::KEYS;
+        constexpr int CB = kv4_codes_bytes(C::KEYS, D), SB = kv4_scales_bytes(C::KEYS, D);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const uint8_t* half = src + v * kv4_half_bytes((int)P, D);
+          const uint8_t* half = src + v * kv4_half_bytes(P, D);
           bulk_load(dst + v * (CB + SB), half + kv4_codes_bytes(o, D), CB, bar);
-          bulk_load(dst + v * (CB + SB) + CB, half + kv4_codes_bytes((int)P, D) + kv4_scales_bytes(o, D), SB, bar);
+          bulk_load(dst + v * (CB + SB) + CB, half + kv4_codes_bytes(P, D) + kv4_scales_bytes(o, D), SB, bar);
         }
       }
     }
@@ -143,7 +159,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int m = a.first + nt * 8 + g;
-    const bool live = m < a.n;
+    const bool live = m < a.n && h < p.Hkv;
     const __nv_bfloat16* q = p.Q + (a.q0 + m / p.share) * p.ldq + ((long long)h * p.share + m % p.share) * D;
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
@@ -170,15 +186,15 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
   }
 
-  // the warp's chunks: c_lo + warp, then every fourth; the ring is filled ahead, page numbers one
-  // chunk further ahead still
-  int c_issue = c_lo + warp;
+  // the warp's stages: c_lo + part, then every per_item-th; the ring is filled ahead, page numbers one
+  // stage further ahead still
+  int c_issue = c_lo + part;
   int st_issue = 0;
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
     if (c_issue < c_hi) {
       issue(c_issue, st_issue, page_of(c_issue));
-      c_issue += KA_WARPS;
+      c_issue += p.per_item;
       ++st_issue;
     }
   }
@@ -187,38 +203,55 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   int st = 0;
   uint32_t phase = 0;
   bool alive = true;
-  const int key_row = (g >> 1) + 4 * (g & 1);
-  for (int c = c_lo + warp; c < c_hi; c += KA_WARPS) {
+  for (int c = c_lo + part; c < c_hi; c += p.per_item) {
     if (c_issue < c_hi) {     // into the stage read in the last turn
       __syncwarp();
       issue(c_issue, st_issue, next_page);
       if (++st_issue == C::STAGES) st_issue = 0;
-      c_issue += KA_WARPS;
+      c_issue += p.per_item;
       next_page = page_of(c_issue);
     }
     // after a wait that ran out, what is in flight is still waited for, then the warp leaves
     alive = __all_sync(0xffffffffu, mbar_wait(&bars[warp][st], phase, p.status, nullptr)) && alive;
-    if (alive) {
-      const uint8_t* stage = ring + st * C::STAGE;
-      const int k0 = c * KA_CHUNK;
-      const uint32_t bad = (bad_of >> (4 * st)) & 15u;
-      const bool whole = bad == 0 && k0 + KA_CHUNK <= sees_all && k0 + KA_CHUNK <= a.len;
+    const uint8_t* stage = ring + st * C::STAGE;
+    const uint32_t bad = (bad_of >> (8 * st)) & 255u;
+    // one chunk; WHOLE: every row sees every key of it
+    auto chunk = [&](auto whole_c, int sub) {
+      constexpr bool WHOLE = decltype(whole_c)::value;
+      const int k0 = c * C::KEYS + sub * KA_CHUNK;
+      // the record and the row in it of the 16 keys of score tile t
+      const uint8_t* base0 = stage;
+      int in0 = 0;
+      if (BIG) {
+        base0 = stage + ((sub * KA_CHUNK) >> PE_log2) * rec;
+        in0 = (sub * KA_CHUNK) & (PE - 1);
+      }
+      auto base_of = [&](int t) { return BIG ? base0 : stage + ((sub * KA_CHUNK + 16 * t) >> PE_log2) * rec; };
+      auto in_of = [&](int t) { return BIG ? in0 + 16 * t : (sub * KA_CHUNK + 16 * t) & (PE - 1); };
+      auto lost_of = [&](int t) { return ((bad >> ((sub * KA_CHUNK + 16 * t) >> PE_log2)) & 1u) != 0; };
       float s[4][NT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int piece = (16 * t) >> PE_log2, in = (16 * t) & (PE - 1);
-        const uint8_t* base = stage + piece * rec;
+        const uint8_t* base = base_of(t);
+        const int in = in_of(t);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[t][nt][0] = s[t][nt][1] = s[t][nt][2] = s[t][nt][3] = 0.f;
-        uint32_t w0[KW], w1[KW];
-        const int r0 = in + key_row;
+        uint32_t w0[KW], w1[KW], s0, s1;
+        const int r0 = in + ka_key<D>(g), r1 = in + ka_key<D>(g + 8);
         ka_words<KW>(base + r0 * (D / 2) + tq * (4 * KW), w0);
-        ka_words<KW>(base + (r0 + 8) * (D / 2) + tq * (4 * KW), w1);
+        ka_words<KW>(base + r1 * (D / 2) + tq * (4 * KW), w1);
         const uint16_t* sc = reinterpret_cast<const uint16_t*>(base + kv4_codes_bytes(PE, D));
-        const int grp = (tq * KW) >> 2;
-        uint32_t s0 = sc[r0 * (D / 32) + grp], s1 = sc[(r0 + 8) * (D / 32) + grp];
-        s0 |= s0 << 16;
-        s1 |= s1 << 16;
+        if (D == 32) {           // keys 2g and 2g + 1: their scales are one word
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(sc + r0);
+          s0 = __byte_perm(x, x, 0x1010);
+          s1 = __byte_perm(x, x, 0x3232);
+        } else {
+          const int grp = (tq * KW) >> 2;
+          s0 = sc[r0 * (D / 32) + grp];
+          s1 = sc[r1 * (D / 32) + grp];
+          s0 = __byte_perm(s0, s0, 0x1010);
+          s1 = __byte_perm(s1, s1, 0x1010);
+        }
         const uint32_t f0 = kv4_offset(s0), f1 = kv4_offset(s1);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
@@ -236,45 +269,58 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
           }
         }
       }
-      if (!whole) {
+      if (!WHOLE) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const bool lost = (bad >> ((16 * t) >> PE_log2)) & 1u;
-          const int j = k0 + 16 * t + key_row;
+          const bool lost = lost_of(t);
+          const int j = k0 + 16 * t;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (lost || j + 8 * (e >> 1) >= limit[nt][e & 1]) s[t][nt][e] = -INFINITY;
+              if (lost || j + ka_key<D>(g + 8 * (e >> 1)) >= limit[nt][e & 1]) s[t][nt][e] = -INFINITY;
         }
       }
-      // running maximum and sum of each query column; P^T in the operand's layout
+      // each query column's maximum; the reference moves, and what was summed against it is rescaled,
+      // where a weight would exceed 2^8
+      bool moves = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+          for (int t = 1; t < 4; ++t) m = fmax3(m, s[t][nt][e], s[t][nt][e + 2]);
+          mx[nt][e] = m * p.sl2;
+          moves = moves || mx[nt][e] > m_run[nt][e] + kKaLazyLog2;
+        }
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], x));
+            const float m_new = fmaxf(m_run[nt][e], mx[nt][e]);
+            corr[e] = m_new == -INFINITY ? 1.f : ex2_approx(m_run[nt][e] - m_new);
+            m_run[nt][e] = m_new;
+            l_run[nt][e] *= corr[e];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
+        }
+      }
+      // weights and their sums; P^T in the operand's layout
       uint32_t pf[4][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float mx[2];
+        float neg[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
-#pragma unroll
-          for (int t = 1; t < 4; ++t) mx[e] = fmaxf(mx[e], fmaxf(s[t][nt][e], s[t][nt][e + 2]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
-        }
-        float neg[2], corr[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float m_new = fmaxf(m_run[nt][e], mx[e] * p.sl2);
-          const float ref = m_new == -INFINITY ? 0.f : m_new;    // nothing seen yet: every exponential is 0
-          corr[e] = ex2_approx(m_run[nt][e] - ref);
-          neg[e] = -ref;
-          m_run[nt][e] = m_new;
-          l_run[nt][e] *= corr[e];
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
+        for (int e = 0; e < 2; ++e) neg[e] = m_run[nt][e] == -INFINITY ? 0.f : -m_run[nt][e];   // nothing seen yet: weights of 0
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           float e4[4];
@@ -289,32 +335,41 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       // O^T += V^T P^T
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int piece = (16 * t) >> PE_log2, in = (16 * t) & (PE - 1);
-        const uint8_t* base = stage + piece * rec + kv4_half_bytes(PE, D);
+        const uint8_t* base = base_of(t) + kv4_half_bytes(PE, D);
+        const int in = in_of(t);
         const int word = D >= 64 ? g * VW : (g & 3), grp = word >> 2;
-        const int pre = D >= 64 ? 0 : 8 * (g >> 2);    // d = 32: lanes 4 apart share a word
-        uint32_t vw[4][VW], vs[4];
+        // the lane's keys: operand columns 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+        const int col[4] = {2 * tq, 2 * tq + 1, 2 * tq + 8, 2 * tq + 9};
+        uint32_t vw[4][VW], sa, sb;
         const uint16_t* sc = reinterpret_cast<const uint16_t*>(base + kv4_codes_bytes(PE, D));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = in + tq + 4 * i;
-          ka_words<VW>(base + r * (D / 2) + word * 4, vw[i]);
-          vs[i] = sc[r * (D / 32) + grp];
+        for (int i = 0; i < 4; ++i) ka_words<VW>(base + (in + ka_key<D>(col[i])) * (D / 2) + word * 4, vw[i]);
+        if (D == 32) {           // keys 4 tq .. 4 tq + 3, in the order 0, 2, 1, 3
+          const uint2 x = *reinterpret_cast<const uint2*>(sc + in + 4 * tq);
+          sa = __byte_perm(x.x, x.y, 0x5410);
+          sb = __byte_perm(x.x, x.y, 0x7632);
+        } else {
+          uint32_t vs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs[i] = sc[(in + ka_key<D>(col[i])) * (D / 32) + grp];
+          sa = __byte_perm(vs[0], vs[1], 0x5410);
+          sb = __byte_perm(vs[2], vs[3], 0x5410);
         }
-        if (!whole) {
+        if (!WHOLE) {
           // a key that does not exist has a weight of zero, but what lies in its place may be
           // anything: its value is made zero too
-          const bool lost = (bad >> piece) & 1u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (lost || k0 + 16 * t + tq + 4 * i >= a.len) vs[i] = 0;
+          const int left = lost_of(t) ? 0 : a.len - (k0 + 16 * t);
+          sa &= (ka_key<D>(col[0]) < left ? 0xffffu : 0u) | (ka_key<D>(col[1]) < left ? 0xffff0000u : 0u);
+          sb &= (ka_key<D>(col[2]) < left ? 0xffffu : 0u) | (ka_key<D>(col[3]) < left ? 0xffff0000u : 0u);
         }
-        const uint32_t sa = vs[0] | (vs[1] << 16), sb = vs[2] | (vs[3] << 16);
         const uint32_t fa = kv4_offset(sa), fb = kv4_offset(sb);
+        // nibbles i (lo) and 4 + i (hi) of two keys' words as pairs; with d = 32 lanes 4 apart share a
+        // word and take nibbles 0, 1 and 4, 5 or 2, 3 and 6, 7 of it
+        const uint32_t lo = D >= 64 ? 0x5410u : g < 4 ? 0x0400u : 0x0501u, hi = D >= 64 ? 0x7632u : g < 4 ? 0x0602u : 0x0703u;
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          const uint32_t la = __byte_perm(vw[0][w], vw[1][w], 0x5410) >> pre, ha = __byte_perm(vw[0][w], vw[1][w], 0x7632) >> pre;
-          const uint32_t lb = __byte_perm(vw[2][w], vw[3][w], 0x5410) >> pre, hb = __byte_perm(vw[2][w], vw[3][w], 0x7632) >> pre;
+          const uint32_t la = __byte_perm(vw[0][w], vw[1][w], lo), ha = __byte_perm(vw[0][w], vw[1][w], hi);
+          const uint32_t lb = __byte_perm(vw[2][w], vw[3][w], lo), hb = __byte_perm(vw[2][w], vw[3][w], hi);
 #pragma unroll
           for (int i = 0; i < VN; ++i) {
             const uint32_t av[4] = {kv4_fma2(kv4_pair(la >> (4 * i)), sa, fa), kv4_fma2(kv4_pair(ha >> (4 * i)), sa, fa),
@@ -324,6 +379,13 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
           }
         }
       }
+    };
+#pragma unroll 1
+    for (int sub = 0; sub < C::KEYS / KA_CHUNK; ++sub) {
+      const int k0 = c * C::KEYS + sub * KA_CHUNK;
+      if (!alive || k0 >= seen) break;
+      if (bad == 0 && k0 + KA_CHUNK <= sees_all && k0 + KA_CHUNK <= a.len) chunk(std::true_type{}, sub);
+      else chunk(std::false_type{}, sub);
     }
     if (++st == C::STAGES) {
       st = 0;
@@ -331,7 +393,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
     }
   }
 
-  // join the warps: outputs through the ring's memory
+  // join an item's warps: outputs through the ring's memory
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -357,31 +419,31 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
         so[(warp * T + nt * 8 + 2 * tq + (e & 1)) * D + d0 + 4 * (e >> 1)] = o[mt][nt][e];
   }
   __syncthreads();
-  const long long item = ((long long)blockIdx.x * p.Hkv + h) * p.n_split + blockIdx.z;
-  for (int i = threadIdx.x; i < T * (D / 2); i += KA_WARPS * 32) {
-    const int row = i / (D / 2), d = 2 * (i % (D / 2));
-    const int m = a.first + row;
-    if (m >= a.n) break;
-    float top = s_m[0][row];
-#pragma unroll
-    for (int w = 1; w < KA_WARPS; ++w) top = fmaxf(top, s_m[w][row]);
+  const int live = min(T, a.n - a.first);
+  for (int i = threadIdx.x; i < heads * live * (D / 2); i += KA_WARPS * 32) {
+    const int d = 2 * (i % (D / 2)), hr = i / (D / 2), hi = hr / live, row = hr - hi * live;
+    const int hh = blockIdx.y * heads + hi, w0 = hi * p.per_item;
+    if (hh >= p.Hkv) break;
+    float top = s_m[w0][row];
+    for (int w = 1; w < p.per_item; ++w) top = fmaxf(top, s_m[w0 + w][row]);
     const float ref = top == -INFINITY ? 0.f : top;
     float l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < KA_WARPS; ++w) {
-      const float f = ex2_approx(s_m[w][row] - ref);
-      const float2 v = *reinterpret_cast<const float2*>(so + (w * T + row) * D + d);
-      l = fmaf(f, s_l[w][row], l);
+    for (int w = 0; w < p.per_item; ++w) {
+      const float f = ex2_approx(s_m[w0 + w][row] - ref);
+      const float2 v = *reinterpret_cast<const float2*>(so + ((w0 + w) * T + row) * D + d);
+      l = fmaf(f, s_l[w0 + w][row], l);
       x = fmaf(f, v.x, x);
       y = fmaf(f, v.y, y);
     }
+    const int m = a.first + row;
     if (p.n_split == 1) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;      // a row that sees nothing is zero
-      __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
+      __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)hh * p.share + m % p.share) * D + d;
       *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
     } else {
-      *reinterpret_cast<float2*>(p.part + (item * T + row) * D + d) = make_float2(x, y);
-      if (d == 0) p.part_ml[item * T + row] = make_float2(top, l);
+      const long long at = ((((long long)blockIdx.x * p.Hkv + hh) * p.n_split + blockIdx.z) * T + row);
+      *reinterpret_cast<float2*>(p.part + at * D + d) = make_float2(x, y);
+      if (d == 0) p.part_ml[at] = make_float2(top, l);
     }
   }
 }
@@ -468,6 +530,7 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, in
 // How a call is laid out: rows per tile, an upper bound of its tiles, and the key splits.
 struct KaPlan {
   int NT = 1, T = 8, n_split = 1;   // NT = 0: the tcgen05 kernel
+  int per_item = KA_WARPS;          // warps a (tile, head)
   long long tiles = 0;
   size_t part_bytes = 0, bytes = 0;
 };
@@ -481,15 +544,20 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
   k.T = k.NT > 0 ? 8 * k.NT : 128;
   k.tiles = packed / k.T + B_R;
-  // fill about twice the resident blocks (four an SM); a split has at least four chunks a warp
-  const long long busy = (packed + k.T - 1) / k.T;
+  // about as many tiles as will have rows: a request's rows begin a tile of their own
+  const long long full = packed / k.T, own = rows < B_R ? rows : B_R;
+  const long long busy = full > own ? full : own;
   const long long items = (busy < 1 ? 1 : busy) * d.H_kv;
-  const long long want = (k.NT > 0 ? KA_WANT : KT_WANT) * ctx->num_sms;
+  // the keys are split until the blocks fill the GPU once (three an SM with d = 128, else four; two or
+  // three of the 128-row kernel's), not beyond: a second, partly filled wave costs more
+  const long long slots = (k.NT > 0 ? (d.d_h == 128 ? 3LL : 4LL) : d.d_h == 32 ? 3LL : 2LL) * ctx->num_sms;
   const long long longest = ((long long)max_blocks * d.page_size + KA_CHUNK - 1) / KA_CHUNK;
-  long long split = items >= want / 2 ? 1 : want / items;
+  long long split = slots / items;
   const long long most = longest / (k.NT > 0 ? 4 * KA_WARPS : 8);
   split = split > most ? most : split;
   k.n_split = (int)(split < 1 ? 1 : split > 1024 ? 1024 : split);
+  // items alone fill the GPU's warps (16 an SM) once over: fewer warps an item
+  k.per_item = items >= KA_FULL * ctx->num_sms ? 1 : items >= KA_FULL / 2 * ctx->num_sms ? 2 : 4;
   if (k.n_split > 1) {
     const size_t n = (size_t)k.tiles * d.H_kv * k.n_split * k.T;
     k.part_bytes = (n * d.d_h * 4 + 255) / 256 * 256;
@@ -507,23 +575,30 @@ rocs_status ka_join(const KaParams& p, const KaPlan& k, cudaStream_t s) {
   return cuda_check(cudaGetLastError(), "attn_kv4_join_kernel");
 }
 
-template <int D, int NT>
+template <int D, int NT, bool BIG>
 rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
   using C = KaCfg<D>;
   static_assert(C::SMEM >= KA_WARPS * 8 * NT * D * 4, "the join's outputs fit the ring");
   static bool attr[64] = {false};
   if (C::SMEM > 48 * 1024 && (ctx->device >= 64 || !attr[ctx->device])) {
-    rocs_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    rocs_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_kernel<D, NT, BIG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      C::SMEM), "cudaFuncSetAttribute(attn_kv4)");
     if (st != ROCS_OK) return st;
     if (ctx->device < 64) attr[ctx->device] = true;
   }
   {
     LaunchTimer lt_("attn_kv4", s);
-    attn_kv4_kernel<D, NT><<<dim3((unsigned)k.tiles, p.Hkv, k.n_split), KA_WARPS * 32, C::SMEM, s>>>(p);
+    const int heads = KA_WARPS / k.per_item;
+    attn_kv4_kernel<D, NT, BIG>
+        <<<dim3((unsigned)k.tiles, (p.Hkv + heads - 1) / heads, k.n_split), KA_WARPS * 32, C::SMEM, s>>>(p);
   }
   rocs_status st = cuda_check(cudaGetLastError(), "attn_kv4_kernel");
   return st != ROCS_OK || k.n_split == 1 ? st : ka_join<D, 8 * NT>(p, k, s);
+}
+
+template <int D, int NT>
+rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  return p.P_log2 >= 6 ? ka_launch<D, NT, true>(ctx, p, k, s) : ka_launch<D, NT, false>(ctx, p, k, s);
 }
 
 template <int D>
@@ -572,6 +647,7 @@ rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const voi
   p.O = (__nv_bfloat16*)O;
   p.ldo = ldo;
   p.n_split = k.n_split;
+  p.per_item = k.per_item;
   p.part = (float*)scratch;
   p.part_ml = (float2*)((char*)scratch + k.part_bytes);
   p.status = ctx->d_status;

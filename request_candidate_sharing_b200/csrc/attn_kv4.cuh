@@ -25,6 +25,7 @@ struct KaParams {
   __nv_bfloat16* O;
   long long ldo;
   int n_split;
+  int per_item;         // warps a (tile, head) of the kernel for few rows
   float* part;          // [tile][head][split][row][D] sums, then [tile][head][split][row] (max, sum) pairs
   float2* part_ml;
   int* status;
