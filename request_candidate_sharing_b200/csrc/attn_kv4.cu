@@ -33,20 +33,17 @@
 namespace rocs {
 namespace {
 
-#ifndef KA_FULL
-#define KA_FULL 16LL
-#endif
 constexpr int KA_WARPS = 4;
 constexpr int kTcRows = 32;     // packed rows a request above which the 128-row tensor-core tiles pay
-constexpr int KA_CHUNK = 64;    // keys scored at a time
 constexpr float kKaLazyLog2 = 8.0f;   // a row's reference maximum moves when a chunk exceeds it by this much
 
 template <int D>
 struct KaCfg {
-  static constexpr int KEYS = D == 32 ? 128 : 64;          // keys per stage of a warp's ring
-  static constexpr int KEYS_LOG2 = D == 32 ? 7 : 6;
+  static constexpr int KEYS_LOG2 = D == 32 ? 7 : 6;          // keys per stage of a warp's ring
+  static constexpr int KEYS = 1 << KEYS_LOG2;
+  static constexpr int CHUNK = 64;                           // keys scored at a time
   static constexpr int STAGE = KEYS * D * 9 / 8;
-  static constexpr int STAGES = D == 128 ? 2 : 3;
+  static constexpr int STAGES = D == 64 ? 3 : 2;
   static constexpr int RING = STAGE * STAGES;
   static constexpr int SMEM = KA_WARPS * RING;
 };
@@ -140,8 +137,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       const uint8_t* src = head + page * page_bytes;
       if (p.P_log2 <= C::KEYS_LOG2) {
         bulk_load(dst, src, rec, bar);
-      } else {                            // half of a 128-token page: its four parts one by one
-        const int P = 1 << p.P_log2, o = (c & 1) * C::KEYS;
+      } else {                            // part of a page: codes and scales of keys and values one by one
+        const int P = 1 << p.P_log2, o = (c * C::KEYS) & (P - 1);
         constexpr int CB = kv4_codes_bytes(C::KEYS, D), SB = kv4_scales_bytes(C::KEYS, D);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -218,20 +215,21 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
     // one chunk; WHOLE: every row sees every key of it
     auto chunk = [&](auto whole_c, int sub) {
       constexpr bool WHOLE = decltype(whole_c)::value;
-      const int k0 = c * C::KEYS + sub * KA_CHUNK;
+      const int k0 = c * C::KEYS + sub * C::CHUNK;
       // the record and the row in it of the 16 keys of score tile t
       const uint8_t* base0 = stage;
       int in0 = 0;
       if (BIG) {
-        base0 = stage + ((sub * KA_CHUNK) >> PE_log2) * rec;
-        in0 = (sub * KA_CHUNK) & (PE - 1);
+        base0 = stage + ((sub * C::CHUNK) >> PE_log2) * rec;
+        in0 = (sub * C::CHUNK) & (PE - 1);
       }
-      auto base_of = [&](int t) { return BIG ? base0 : stage + ((sub * KA_CHUNK + 16 * t) >> PE_log2) * rec; };
-      auto in_of = [&](int t) { return BIG ? in0 + 16 * t : (sub * KA_CHUNK + 16 * t) & (PE - 1); };
-      auto lost_of = [&](int t) { return ((bad >> ((sub * KA_CHUNK + 16 * t) >> PE_log2)) & 1u) != 0; };
-      float s[4][NT][4];
+      auto base_of = [&](int t) { return BIG ? base0 : stage + ((sub * C::CHUNK + 16 * t) >> PE_log2) * rec; };
+      auto in_of = [&](int t) { return BIG ? in0 + 16 * t : (sub * C::CHUNK + 16 * t) & (PE - 1); };
+      auto lost_of = [&](int t) { return ((bad >> ((sub * C::CHUNK + 16 * t) >> PE_log2)) & 1u) != 0; };
+      constexpr int ST = C::CHUNK / 16;      // score tiles
+      float s[ST][NT][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < ST; ++t) {
         const uint8_t* base = base_of(t);
         const int in = in_of(t);
 #pragma unroll
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       }
       if (!WHOLE) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < ST; ++t) {
           const bool lost = lost_of(t);
           const int j = k0 + 16 * t;
 #pragma unroll
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
         for (int e = 0; e < 2; ++e) {
           float m = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
 #pragma unroll
-          for (int t = 1; t < 4; ++t) m = fmax3(m, s[t][nt][e], s[t][nt][e + 2]);
+          for (int t = 1; t < ST; ++t) m = fmax3(m, s[t][nt][e], s[t][nt][e + 2]);
           mx[nt][e] = m * p.sl2;
           moves = moves || mx[nt][e] > m_run[nt][e] + kKaLazyLog2;
         }
@@ -315,14 +313,14 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
         }
       }
       // weights and their sums; P^T in the operand's layout
-      uint32_t pf[4][NT][2];
+      uint32_t pf[ST][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float neg[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) neg[e] = m_run[nt][e] == -INFINITY ? 0.f : -m_run[nt][e];   // nothing seen yet: weights of 0
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < ST; ++t) {
           float e4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4[e] = ex2_approx(fmaf(s[t][nt][e], p.sl2, neg[e & 1]));
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       }
       // O^T += V^T P^T
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < ST; ++t) {
         const uint8_t* base = base_of(t) + kv4_half_bytes(PE, D);
         const int in = in_of(t);
         const int word = D >= 64 ? g * VW : (g & 3), grp = word >> 2;
@@ -381,10 +379,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       }
     };
 #pragma unroll 1
-    for (int sub = 0; sub < C::KEYS / KA_CHUNK; ++sub) {
-      const int k0 = c * C::KEYS + sub * KA_CHUNK;
+    for (int sub = 0; sub < C::KEYS / C::CHUNK; ++sub) {
+      const int k0 = c * C::KEYS + sub * C::CHUNK;
       if (!alive || k0 >= seen) break;
-      if (bad == 0 && k0 + KA_CHUNK <= sees_all && k0 + KA_CHUNK <= a.len) chunk(std::true_type{}, sub);
+      if (bad == 0 && k0 + C::CHUNK <= sees_all && k0 + C::CHUNK <= a.len) chunk(std::true_type{}, sub);
       else chunk(std::false_type{}, sub);
     }
     if (++st == C::STAGES) {
@@ -541,7 +539,7 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   const long long packed = rows * share;
   // as many packed rows per tile as a request has on average
   const double avg = (double)packed / B_R;
-  k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
+    k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
   k.T = k.NT > 0 ? 8 * k.NT : 128;
   k.tiles = packed / k.T + B_R;
   // about as many tiles as will have rows: a request's rows begin a tile of their own
@@ -551,13 +549,14 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   // the keys are split until the blocks fill the GPU once (three an SM with d = 128, else four; two or
   // three of the 128-row kernel's), not beyond: a second, partly filled wave costs more
   const long long slots = (k.NT > 0 ? (d.d_h == 128 ? 3LL : 4LL) : d.d_h == 32 ? 3LL : 2LL) * ctx->num_sms;
-  const long long longest = ((long long)max_blocks * d.page_size + KA_CHUNK - 1) / KA_CHUNK;
+  const long long longest = ((long long)max_blocks * d.page_size + 63) / 64;
   long long split = slots / items;
   const long long most = longest / (k.NT > 0 ? 4 * KA_WARPS : 8);
   split = split > most ? most : split;
   k.n_split = (int)(split < 1 ? 1 : split > 1024 ? 1024 : split);
-  // items alone fill the GPU's warps (16 an SM) once over: fewer warps an item
-  k.per_item = items >= KA_FULL * ctx->num_sms ? 1 : items >= KA_FULL / 2 * ctx->num_sms ? 2 : 4;
+  // one warp an item where items fill the GPU's warps (16 an SM) more than once, two where they nearly do:
+  // 41 instead of 57 us on 4096 items of 500 keys (d = 32), 42 instead of 46 us on 1200 with four warps (d = 64)
+  k.per_item = items >= 24LL * ctx->num_sms ? 1 : items >= 12LL * ctx->num_sms ? 2 : 4;
   if (k.n_split > 1) {
     const size_t n = (size_t)k.tiles * d.H_kv * k.n_split * k.T;
     k.part_bytes = (n * d.d_h * 4 + 255) / 256 * 256;
