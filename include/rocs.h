@@ -358,10 +358,11 @@ rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc
  * A request whose lengths are negative or exceed max_blocks * P tokens, or whose pages exceed what
  * free_pages still holds, takes none: its rows (new_len of them, none if negative) get -1, its kv_len
  * stays past_len (0 if past_len itself is unusable) and the device status becomes ROCS_ERR_COUNTS;
- * new rows that sum to more than `rows` set it too (those beyond are not written).  A page outside
- * [0, n_pages), in the table or the free list, gives its rows -1 and sets ROCS_ERR_INDEX.
+ * new rows that sum to more than `rows` set it too (those beyond are not written, nor the table entries
+ * of pages that begin in them).  A page outside [0, n_pages), in the table or the free list, gives its
+ * rows -1 and sets ROCS_ERR_INDEX.
  * The outputs may not overlap the inputs or one another.
- * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 4096
+ * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 2048
  * requests), 16-byte aligned.  Limits: 1 <= B_R <= 2^24; 0 <= rows < 2^31 - 1; 0 <= n_free < 2^31 - 1;
  * max_blocks >= 1 with max_blocks * P <= 2^31 - 256; page_size 16, 32, 64 or 128. */
 rocs_status rocs_kv_block_tables_workspace(rocs_handle_t handle, int32_t B_R, size_t* bytes);

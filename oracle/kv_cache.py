@@ -35,6 +35,8 @@ def block_tables(past, new, page, free, n_pages, table, rows):
         if ok and fits:
             first = math.ceil(p / page)
             for b in range(need):
+                if row + (first + b) * page - p >= rows:
+                    break                        # the page begins in a row that is not there
                 if 0 <= free[taken + b] < n_pages:
                     table[r, first + b] = free[taken + b]
                 else:

@@ -455,7 +455,10 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, in
   constexpr int GROUPS = 256 / D;
   __shared__ float s_part[GROUPS][D + 2];
   KaTile a;
-  if (!ka_tile(p, blockIdx.x, T, a)) return;
+  // (offsets and lengths are the caller's, not the launch's before this one)
+  const bool has = ka_tile(p, blockIdx.x, T, a);
+  grid_dependency_wait();
+  if (!has) return;
   const int h = blockIdx.y, grp = threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
   const bool shared_row = p.n_split > KJ_SPLITS;
   const int row_step = shared_row ? 1 : GROUPS, split_step = shared_row ? GROUPS : 1;
@@ -570,8 +573,8 @@ rocs_status ka_join(const KaParams& p, const KaPlan& k, cudaStream_t s) {
   LaunchTimer lt_("attn_kv4_join", s);
   // a block takes one row of many splits, or 16 rows of a few
   const int rows = k.n_split > KJ_SPLITS ? 1 : T < 16 ? T : 16;
-  attn_kv4_join_kernel<D, T><<<dim3((unsigned)k.tiles, p.Hkv, T / rows), 128, 0, s>>>(p, rows);
-  return cuda_check(cudaGetLastError(), "attn_kv4_join_kernel");
+  return launch_dependent(attn_kv4_join_kernel<D, T>, dim3((unsigned)k.tiles, p.Hkv, T / rows), dim3(128), 0, s, "attn_kv4_join_kernel",
+                          p, rows);
 }
 
 template <int D, int NT, bool BIG>

@@ -83,6 +83,24 @@ rocs_status cuda_check(cudaError_t e, const char* what);
 // prefixed with `who`, the entry point's name.
 rocs_status check_ikbo_desc(const rocs_ikbo_desc* d, const char* who);
 
+// Launches a kernel that begins with grid_dependency_wait(): it is set up while the launch before it in
+// the stream still runs, which hides the launch latency between the two.
+template <typename... Params, typename... Args>
+rocs_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const char* what,
+                             Args... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&c, kernel, args...), what);
+}
+
 // One GEMM problem for the tcgen05 kernel:
 //   out[r, c] = act( scale[c] * sum_k A[r, k] * B[c, k] + bias[c] + Z[gidx[r], c] )
 // A [M, K] bf16 (row stride lda), B [N, K] bf16 (row stride ldb); bias, Z, gidx optional.
@@ -254,7 +272,7 @@ rocs_status launch_attention_tc(rocs_context* ctx, const void* Q, long long ldq,
                                 int q_by_kv = 0, const int32_t* order = nullptr);
 
 // The 4-bit history cache.  Block tables and slot maps (kv_tables.cu): scratch of
-// kv_tables_scratch(B_R) bytes (0 up to 4096 requests).
+// kv_tables_scratch(B_R) bytes (0 up to 2048 requests).
 size_t kv_tables_scratch(int B_R);
 rocs_status launch_kv_tables(rocs_context* ctx, const int32_t* past, const int32_t* fresh_len, int B_R, int page_log2,
                              const int32_t* free_pages, int n_free, int n_pages, int32_t* table, int max_blocks,

@@ -9,11 +9,15 @@
 //
 // Up to kTabInline requests every block computes both totals by itself in shared memory (two reads of
 // 4 B a request from L2, one block-wide scan): one launch instead of three, and the decode step (512
-// requests, 512 rows) is all launch latency.  Beyond, a block per kTabInline requests totals its
-// part, a second launch scans and writes the totals, a third expands.  Expansion is by output row,
-// four neighbouring rows a thread (16-byte stores), each thread finding its first row's request by
-// binary search and walking on; so one request with a million rows spreads over the whole GPU.
-// Bound by the 12 bytes written per row.
+// requests, 512 rows) is all launch latency.  Beyond, a block per kTabThreads requests totals its
+// part, a second launch scans and writes the totals, a third expands.  Expansion is by output row, so one request with a million rows spreads over the whole GPU; a warp takes
+// neighbouring rows, and each lane finds its first row's request by binary search in shared memory and
+// walks on (four neighbouring rows a lane, with wide stores, diverged in every warp: 64 us instead of
+// TABBEST for 7.2 M rows).
+// A fresh page's table entry is written by the thread of the page's first row.  Past kTabInline requests
+// a block takes a tile of neighbouring rows, finds its first request by two block-wide probes and brings
+// the requests from there on into shared memory (a search per thread in L2 took most of 90 us for 7.2 M
+// rows of 40000 requests).  Bound by the 12 bytes written per row.
 #include "common.cuh"
 #include "internal.h"
 
@@ -21,8 +25,9 @@ namespace rocs {
 namespace {
 
 constexpr int kTabThreads = 512;
-constexpr int kTabItems = 8;                              // requests per thread of a scan
-constexpr int kTabInline = kTabThreads * kTabItems;       // 4096
+constexpr int kTabItems = 4;                              // requests per thread of a scan
+constexpr int kTabInline = kTabThreads * kTabItems;       // 2048
+constexpr int kTabRows = 4;                               // rows a thread of a tile, scanned by every block
 
 struct TabParams {
   const int32_t *past, *fresh_len;   // past may be null: nothing is cached
@@ -37,8 +42,9 @@ struct TabParams {
   int32_t* positions;
   long long rows;
   int32_t* pages_used;
-  long long* part;        // [2 * chunks]: rows and pages of each chunk of kTabInline requests
+  long long* part;        // [2 * chunks]: rows and pages of each chunk of kTabThreads requests
   long long* page_off;    // [B_R + 1]
+  int tile_rows;          // rows a thread of a tile, otherwise
   int* status;
 };
 
@@ -103,70 +109,56 @@ __device__ __forceinline__ int tab_owner(const T* off, int lo, int hi, long long
   return lo;
 }
 
-// Rows [4 i, 4 i + 4) and free-list entries of this block, given the running totals of requests
-// [0, B_R): row(r) and page(r) (with their ends at r = B_R).
-template <typename RowT, typename PageT>
-__device__ __forceinline__ void tab_expand(const TabParams& p, const RowT* row_off, const PageT* page_off,
-                                           long long n_rows, long long n_fresh) {
+// Requests [first, first + n) in shared memory: running totals of rows and pages (one more of the rows,
+// the end), and the tokens each holds (-1: it gets no slots).
+struct TabWindow {
+  const int32_t *row, *page, *past;
+  int first, n;
+};
+
+// Rows base + lane, base + lane + 32, .. (count of them): a lane finds its first row's request by binary
+// search and walks on from there.
+__device__ __forceinline__ void tab_rows(const TabParams& p, const TabWindow& w, long long base, int count, long long n_rows) {
   const int mask = (1 << p.P_log2) - 1;
-  const long long stride = (long long)gridDim.x * blockDim.x;
-  const long long first = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  // fresh pages into the table
-  const long long usable = n_fresh < p.n_free ? n_fresh : (long long)p.n_free;
-  for (long long i = first; i < usable; i += stride) {
-    const int r = tab_owner(page_off, 0, p.B_R, i);
-    if ((long long)page_off[r + 1] > p.n_free) continue;   // the free list ran out inside this request
-    const TabReq q = tab_request(p, r);
-    const int page = p.free_pages[i];
-    if (page < 0 || page >= p.n_pages) {
-      set_status(p.status, ROCS_ERR_INDEX);
-      continue;
-    }
-    p.table[(long long)r * p.max_blocks + q.before + (int)(i - (long long)page_off[r])] = page;
-  }
-  // rows
-  for (long long i0 = 4 * first; i0 < p.rows; i0 += 4 * stride) {
-    int64_t sl[4];
-    int32_t po[4];
-    int r = -1;
-    TabReq q;
-    long long row0 = 0, row1 = 0, page0 = 0;
-    bool dead = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const long long i = i0 + e;
-      sl[e] = -1;
-      po[e] = -1;
-      if (i >= p.rows || i >= n_rows) continue;   // a padded batch's rows have no slot
-      if (r < 0 || i >= row1) {
-        r = tab_owner(row_off, r < 0 ? 0 : r, p.B_R, i);
-        q = tab_request(p, r);
-        row0 = row_off[r];
-        row1 = row_off[r + 1];
-        page0 = page_off[r];
-        dead = q.bad || (q.need > 0 && page0 + q.need > p.n_free);
+  int r = -1;                       // the row's request, counted from the window's first
+  for (int k = 0; k < count; ++k) {
+    const long long i = base + (threadIdx.x & 31) + 32 * k;
+    if (i >= p.rows) return;
+    int64_t slot = -1;
+    int pos = -1;
+    if (i < n_rows) {               // a padded batch's rows have no slot
+      long long row0, page0;
+      int past, q = w.n;
+      if (i < w.row[w.n]) {
+        if (r < 0) r = tab_owner(w.row, 0, w.n, i);
+        while (i >= w.row[r + 1]) ++r;
+        q = r;
+        row0 = w.row[r];
+        page0 = w.page[r];
+        past = w.past[r];
+      } else {                      // past the window: thousands of tiny requests in one tile
+        q = tab_owner(p.row_off, w.first + w.n, p.B_R, i) - w.first;
+        const TabReq t = tab_request(p, w.first + q);
+        row0 = p.row_off[w.first + q];
+        page0 = p.page_off[w.first + q];
+        past = t.bad || (t.need > 0 && page0 + t.need > p.n_free) ? -1 : t.past;
       }
-      if (dead) continue;
-      const int pos = q.past + (int)(i - row0);
-      const int blk = pos >> p.P_log2;
-      const int page = blk < q.before ? p.table[(long long)r * p.max_blocks + blk] : p.free_pages[page0 + blk - q.before];
-      if (page < 0 || page >= p.n_pages) {
-        set_status(p.status, ROCS_ERR_INDEX);
-        continue;
-      }
-      sl[e] = ((int64_t)page << p.P_log2) + (pos & mask);
-      po[e] = pos;
-    }
-    if (i0 + 4 <= p.rows) {
-      *reinterpret_cast<longlong2*>(p.slots + i0) = make_longlong2(sl[0], sl[1]);
-      *reinterpret_cast<longlong2*>(p.slots + i0 + 2) = make_longlong2(sl[2], sl[3]);
-      *reinterpret_cast<int4*>(p.positions + i0) = make_int4(po[0], po[1], po[2], po[3]);
-    } else {
-      for (int e = 0; e < 4 && i0 + e < p.rows; ++e) {
-        p.slots[i0 + e] = sl[e];
-        p.positions[i0 + e] = po[e];
+      if (past >= 0) {
+        pos = past + (int)(i - row0);
+        const int blk = pos >> p.P_log2, before = (int)(((unsigned)past + mask) >> p.P_log2);
+        int32_t* entry = p.table + (long long)(w.first + q) * p.max_blocks + blk;
+        const int page = blk >= before ? p.free_pages[page0 + (blk - before)] : *entry;
+        if (page >= 0 && page < p.n_pages) {
+          if (blk >= before && (pos & mask) == 0) *entry = page;
+          slot = ((int64_t)page << p.P_log2) + (pos & mask);
+        } else {
+          set_status(p.status, ROCS_ERR_INDEX);
+          pos = -1;
+        }
       }
     }
+    p.slots[i] = slot;
+    p.positions[i] = pos;
   }
 }
 
@@ -181,49 +173,50 @@ __device__ __forceinline__ long long tab_owner_writes(const TabParams& p, int r,
   return starved || q.need == 0 ? 0 : page + q.need;
 }
 
-// A thread's kTabItems consecutive requests of chunk `base`: their sums.
-__device__ __forceinline__ void tab_items(const TabParams& p, int base, long long& a, long long& b) {
+// A thread's `per` (at most kTabItems) consecutive requests from `base` on: their sums.
+__device__ __forceinline__ void tab_items(const TabParams& p, int base, int per, TabReq (&q)[kTabItems], long long& a,
+                                          long long& b) {
   a = b = 0;
 #pragma unroll
   for (int k = 0; k < kTabItems; ++k) {
-    const int r = base + threadIdx.x * kTabItems + k;
-    if (r < p.B_R) {
-      const TabReq q = tab_request(p, r);
-      a += q.rows;
-      b += q.need;
+    const int r = base + threadIdx.x * per + k;
+    if (k < per && r < p.B_R) {
+      q[k] = tab_request(p, r);
+      a += q[k].rows;
+      b += q[k].need;
     }
   }
 }
 
 __global__ void __launch_bounds__(kTabThreads) kv_tables_inline_kernel(const TabParams p) {
-  __shared__ int32_t s_row[kTabInline + 1];
-  __shared__ int32_t s_page[kTabInline + 1];
+  __shared__ int32_t s_row[kTabInline + 1], s_page[kTabInline], s_past[kTabInline];
   __shared__ int s_used;
   if (threadIdx.x == 0) s_used = 0;
+  const int per = (p.B_R + kTabThreads - 1) / kTabThreads;
+  TabReq q[kTabItems];
   long long a, b, ta, tb;
-  tab_items(p, 0, a, b);
+  tab_items(p, 0, per, q, a, b);
   tab_scan(a, b, &ta, &tb);
   const bool writer = blockIdx.x == 0;
   long long used = 0;
 #pragma unroll
   for (int k = 0; k < kTabItems; ++k) {
-    const int r = threadIdx.x * kTabItems + k;
-    if (r < p.B_R) {
-      const TabReq q = tab_request(p, r);
+    const int r = threadIdx.x * per + k;
+    if (k < per && r < p.B_R) {
       // totals past 2^31 are clipped: such rows and pages lie behind every output
       s_row[r] = clip32(a);
       s_page[r] = clip32(b);
+      s_past[r] = q[k].bad || (q[k].need > 0 && b + q[k].need > p.n_free) ? -1 : q[k].past;
       if (writer) {
-        const long long end = tab_owner_writes(p, r, q, a, b);
+        const long long end = tab_owner_writes(p, r, q[k], a, b);
         used = end > used ? end : used;
       }
-      a += q.rows;
-      b += q.need;
+      a += q[k].rows;
+      b += q[k].need;
     }
   }
   if (threadIdx.x == 0) {
     s_row[p.B_R] = clip32(ta);
-    s_page[p.B_R] = clip32(tb);
   }
   if (writer) {
     if (used > 0) atomicMax(&s_used, (int)used);   // at most n_free
@@ -234,12 +227,104 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_inline_kernel(const Tab
   }
   __syncthreads();
   if (writer && threadIdx.x == 0) *p.pages_used = s_used;
-  tab_expand(p, s_row, s_page, ta, tb);
+  const TabWindow w = {s_row, s_page, s_past, 0, p.B_R};
+  const long long tile = (long long)kTabThreads * kTabRows;
+  for (long long t0 = blockIdx.x * tile; t0 < p.rows; t0 += gridDim.x * tile)
+    tab_rows(p, w, t0 + (threadIdx.x >> 5) * (32 * kTabRows), kTabRows, ta);
+}
+
+// Few rows (at most four a request on average): one block, each request's rows written by its own thread,
+// or by its warp where it has many, without a search; the page that its tokens already end in is asked for
+// before the totals are known.
+constexpr int kTabOwnRows = 4;
+__global__ void __launch_bounds__(kTabThreads) kv_tables_few_kernel(const TabParams p) {
+  __shared__ int s_used;
+  if (threadIdx.x == 0) s_used = 0;
+  const int per = (p.B_R + kTabThreads - 1) / kTabThreads, mask = (1 << p.P_log2) - 1;
+  TabReq q[kTabItems];
+  long long a, b, ta, tb;
+  tab_items(p, 0, per, q, a, b);
+  int32_t open_page[kTabItems];      // the partly filled page, if any
+#pragma unroll
+  for (int k = 0; k < kTabItems; ++k) {
+    const int r = threadIdx.x * per + k;
+    open_page[k] = -1;
+    if (k < per && r < p.B_R && !q[k].bad && q[k].rows > 0 && (q[k].past & mask) != 0)
+      open_page[k] = p.table[(long long)r * p.max_blocks + (q[k].past >> p.P_log2)];
+  }
+  tab_scan(a, b, &ta, &tb);
+  // row j of a request whose rows start at `row` and whose fresh pages start at `page0`
+  auto put = [&](int r, int past, int before, int open, long long page0, long long row, int j) {
+    if (row + j >= p.rows) return;
+    const int pos = past + j, blk = pos >> p.P_log2;
+    const int page = blk >= before ? p.free_pages[page0 + blk - before] : open;
+    const bool ok = page >= 0 && page < p.n_pages;
+    if (!ok) set_status(p.status, ROCS_ERR_INDEX);
+    if (ok && blk >= before && (pos & mask) == 0) p.table[(long long)r * p.max_blocks + blk] = page;
+    p.slots[row + j] = ok ? ((int64_t)page << p.P_log2) + (pos & mask) : -1;
+    p.positions[row + j] = ok ? pos : -1;
+  };
+  long long used = 0;
+#pragma unroll
+  for (int k = 0; k < kTabItems; ++k) {
+    const int r = threadIdx.x * per + k;
+    const bool mine = k < per && r < p.B_R;
+    bool dead = true;
+    int n = 0;
+    if (mine) {
+      const long long end = tab_owner_writes(p, r, q[k], a, b);
+      used = end > used ? end : used;
+      dead = q[k].bad || (q[k].need > 0 && b + q[k].need > p.n_free);
+      n = q[k].rows;
+      if (n <= kTabOwnRows) {
+        for (int j = 0; j < n; ++j) {
+          if (!dead) {
+            put(r, q[k].past, q[k].before, open_page[k], b, a, j);
+          } else if (a + j < p.rows) {
+            p.slots[a + j] = -1;
+            p.positions[a + j] = -1;
+          }
+        }
+      }
+    }
+    for (uint32_t many = __ballot_sync(0xffffffffu, n > kTabOwnRows); many != 0; many &= many - 1) {
+      const int l = __ffs((int)many) - 1;
+      const int wr = __shfl_sync(0xffffffffu, r, l), wn = __shfl_sync(0xffffffffu, n, l);
+      const int wpast = __shfl_sync(0xffffffffu, mine ? q[k].past : 0, l), wbefore = __shfl_sync(0xffffffffu, mine ? q[k].before : 0, l);
+      const int wopen = __shfl_sync(0xffffffffu, open_page[k], l), wdead = __shfl_sync(0xffffffffu, (int)dead, l);
+      const long long wa = __shfl_sync(0xffffffffu, a, l), wb = __shfl_sync(0xffffffffu, b, l);
+      for (long long j = threadIdx.x & 31; j < wn && wa + j < p.rows; j += 32) {
+        if (!wdead) {
+          put(wr, wpast, wbefore, wopen, wb, wa, (int)j);
+        } else {
+          p.slots[wa + j] = -1;
+          p.positions[wa + j] = -1;
+        }
+      }
+    }
+    if (mine) {
+      a += q[k].rows;
+      b += q[k].need;
+    }
+  }
+  // a padded batch's rows have no slot
+  for (long long i = ta + threadIdx.x; i < p.rows; i += kTabThreads) {
+    p.slots[i] = -1;
+    p.positions[i] = -1;
+  }
+  if (used > 0) atomicMax(&s_used, (int)used);   // at most n_free
+  if (threadIdx.x == 0) {
+    p.row_off[p.B_R] = clip32(ta);
+    if (ta > p.rows) set_status(p.status, ROCS_ERR_COUNTS);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) *p.pages_used = s_used;
 }
 
 __global__ void __launch_bounds__(kTabThreads) kv_tables_sum_kernel(const TabParams p) {
+  TabReq q[kTabItems];
   long long a, b, ta, tb;
-  tab_items(p, blockIdx.x * kTabInline, a, b);
+  tab_items(p, blockIdx.x * kTabThreads, 1, q, a, b);
   tab_scan(a, b, &ta, &tb);
   if (threadIdx.x == 0) {
     p.part[2 * blockIdx.x] = ta;
@@ -251,6 +336,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_sum_kernel(const TabPar
 __global__ void __launch_bounds__(kTabThreads) kv_tables_scan_kernel(const TabParams p) {
   __shared__ int s_used;
   if (threadIdx.x == 0) s_used = 0;
+  grid_dependency_wait();
   // the chunks in front of this one
   long long fa = 0, fb = 0, xa, xb;
   for (int c = threadIdx.x; c < (int)blockIdx.x; c += kTabThreads) {
@@ -258,27 +344,22 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_scan_kernel(const TabPa
     fb += p.part[2 * c + 1];
   }
   tab_scan(fa, fb, &xa, &xb);
+  TabReq q[kTabItems];
   long long a, b, ta, tb;
-  tab_items(p, blockIdx.x * kTabInline, a, b);
+  tab_items(p, blockIdx.x * kTabThreads, 1, q, a, b);
   tab_scan(a, b, &ta, &tb);
   a += xa;
   b += xb;
   long long used = 0;
-#pragma unroll
-  for (int k = 0; k < kTabItems; ++k) {
-    const int r = blockIdx.x * kTabInline + threadIdx.x * kTabItems + k;
-    if (r < p.B_R) {
-      const TabReq q = tab_request(p, r);
-      p.page_off[r] = b;
-      const long long end = tab_owner_writes(p, r, q, a, b);
-      used = end > used ? end : used;
-      a += q.rows;
-      b += q.need;
-      if (r == p.B_R - 1) {
-        p.row_off[p.B_R] = clip32(a);
-        p.page_off[p.B_R] = b;
-        if (a > p.rows) set_status(p.status, ROCS_ERR_COUNTS);
-      }
+  const int r = blockIdx.x * kTabThreads + threadIdx.x;
+  if (r < p.B_R) {
+    p.page_off[r] = b;
+    used = tab_owner_writes(p, r, q[0], a, b);
+    if (r == p.B_R - 1) {
+      a += q[0].rows;
+      p.row_off[p.B_R] = clip32(a);
+      p.page_off[p.B_R] = b + q[0].need;
+      if (a > p.rows) set_status(p.status, ROCS_ERR_COUNTS);
     }
   }
   if (used > 0) atomicMax(&s_used, (int)used);
@@ -287,10 +368,36 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_scan_kernel(const TabPa
 }
 
 __global__ void __launch_bounds__(kTabThreads) kv_tables_expand_kernel(const TabParams p) {
-  tab_expand(p, p.row_off, p.page_off, (long long)p.row_off[p.B_R], p.page_off[p.B_R]);
+  __shared__ int32_t s_row[kTabThreads + 1], s_page[kTabThreads], s_past[kTabThreads];
+  grid_dependency_wait();
+  const long long n_rows = p.row_off[p.B_R], tile = (long long)p.tile_rows * kTabThreads;
+  for (long long t0 = blockIdx.x * tile; t0 < p.rows; t0 += gridDim.x * tile) {
+    __syncthreads();            // the window of the tile before is no longer read
+    // the request of the tile's first row: the largest with row_off <= t0, narrowed 512-fold a probe
+    int lo = 0, hi = p.B_R;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + kTabThreads - 1) / kTabThreads;
+      const int r = lo + (int)threadIdx.x * step;
+      const int k = __syncthreads_count(r < hi && (threadIdx.x == 0 || (long long)p.row_off[r] <= t0)) - 1;
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    const int n = min(kTabThreads, p.B_R - lo);
+    if ((int)threadIdx.x < n) {
+      const int r = lo + threadIdx.x;
+      const TabReq q = tab_request(p, r);
+      s_row[threadIdx.x] = p.row_off[r];
+      s_page[threadIdx.x] = clip32(p.page_off[r]);
+      s_past[threadIdx.x] = q.bad || (q.need > 0 && p.page_off[r] + q.need > p.n_free) ? -1 : q.past;
+      if ((int)threadIdx.x == n - 1) s_row[n] = p.row_off[r + 1];
+    }
+    __syncthreads();
+    const TabWindow w = {s_row, s_page, s_past, lo, n};
+    tab_rows(p, w, t0 + (threadIdx.x >> 5) * (32 * p.tile_rows), p.tile_rows, n_rows);
+  }
 }
 
-int tab_chunks(int B_R) { return (B_R + kTabInline - 1) / kTabInline; }
+int tab_chunks(int B_R) { return (B_R + kTabThreads - 1) / kTabThreads; }
 
 }  // namespace
 
@@ -322,10 +429,21 @@ rocs_status launch_kv_tables(rocs_context* ctx, const int32_t* past, const int32
   p.part = (long long*)scratch;
   p.page_off = p.part + 2 * tab_chunks(B_R);
   p.status = ctx->d_status;
-  const long long blocks = (rows + 4LL * kTabThreads - 1) / (4LL * kTabThreads);
-  const long long cap = 4LL * ctx->num_sms;
+  const bool one = B_R <= kTabInline;
+  const long long cap = 4LL * ctx->num_sms;         // resident blocks
+  // enough rows a thread that the tiles are one wave, for the search of a tile's first request is a chain
+  // of latencies
+  const long long per = (rows + kTabThreads * cap - 1) / (kTabThreads * cap);
+  p.tile_rows = (int)(per < kTabRows ? kTabRows : per > 64 ? 64 : per);
+  const long long tile = (long long)kTabThreads * (one ? kTabRows : p.tile_rows);
+  const long long blocks = (rows + tile - 1) / tile;
   const unsigned grid = (unsigned)(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
-  if (B_R <= kTabInline) {
+  if (one && rows <= 4LL * B_R) {
+    LaunchTimer lt_("kv_tables", s);
+    kv_tables_few_kernel<<<1, kTabThreads, 0, s>>>(p);
+    return cuda_check(cudaGetLastError(), "kv_tables_few_kernel");
+  }
+  if (one) {
     LaunchTimer lt_("kv_tables", s);
     kv_tables_inline_kernel<<<grid, kTabThreads, 0, s>>>(p);
     return cuda_check(cudaGetLastError(), "kv_tables_inline_kernel");
@@ -334,13 +452,14 @@ rocs_status launch_kv_tables(rocs_context* ctx, const int32_t* past, const int32
     LaunchTimer lt_("kv_tables_sum", s);
     kv_tables_sum_kernel<<<tab_chunks(B_R), kTabThreads, 0, s>>>(p);
   }
+  rocs_status st;
   {
     LaunchTimer lt_("kv_tables_scan", s);
-    kv_tables_scan_kernel<<<tab_chunks(B_R), kTabThreads, 0, s>>>(p);
+    st = launch_dependent(kv_tables_scan_kernel, dim3(tab_chunks(B_R)), dim3(kTabThreads), 0, s, "kv_tables_scan_kernel", p);
+    if (st != ROCS_OK) return st;
   }
   LaunchTimer lt_("kv_tables_expand", s);
-  kv_tables_expand_kernel<<<grid, kTabThreads, 0, s>>>(p);
-  return cuda_check(cudaGetLastError(), "kv_tables_expand_kernel");
+  return launch_dependent(kv_tables_expand_kernel, dim3(grid), dim3(kTabThreads), 0, s, "kv_tables_expand_kernel", p);
 }
 
 }  // namespace rocs

@@ -73,7 +73,7 @@ def check_tables(R, past, new, page, free, n_pages, table, rows):
 
 @pytest.mark.parametrize("B,page,past_top,new_top,pad", [
     (1, 16, 0, 1, 0), (1, 64, 100, 1, 3), (1, 128, 0, 40001, 7), (3, 16, 17, 33, 0), (512, 64, 1024, 1, 0), (512, 64, 0, 700, 61),
-    (4096, 16, 40, 9, 1), (4097, 16, 40, 9, 0), (9001, 32, 100, 40, 5), (20000, 128, 300, 2, 4000),
+    (2048, 16, 40, 9, 1), (2049, 16, 40, 9, 0), (4096, 16, 40, 9, 1), (4097, 16, 40, 9, 0), (9001, 32, 100, 40, 5), (9000, 32, 100, 1, 5), (20000, 128, 300, 2, 4000),
 ])
 def test_block_tables(R, B, page, past_top, new_top, pad):
     g = np.random.default_rng(B + page)
@@ -90,6 +90,25 @@ def test_block_tables(R, B, page, past_top, new_top, pad):
         table[r, :held[r]] = order[k:k + held[r]]
         k += held[r]
     check_tables(R, past, new, page, order[k:], n_pages, table, int(new.sum()) + pad)
+
+
+@pytest.mark.parametrize("B", [2000, 30000])
+def test_block_tables_many_empty_and_some_long_requests(R, B):
+    """A tile of rows that spans thousands of requests (most get nothing or one row), and one request that
+    spans many tiles."""
+    g = np.random.default_rng(B)
+    new = (g.random(B) < 0.3).astype(np.int64)
+    new[[B // 3, B - 1]] = [30011, 9000]
+    past = g.integers(0, 50, B)
+    page = 16
+    held, after = (past + 15) // 16, (past + new + 15) // 16
+    order = g.permutation(int(after.sum()) + 5).astype(np.int32)
+    table = np.full((B, int(after.max())), -1, np.int32)
+    k = 0
+    for r in range(B):
+        table[r, :held[r]] = order[k:k + held[r]]
+        k += held[r]
+    check_tables(R, past, new, page, order[k:], len(order), table, int(new.sum()) + 3)
 
 
 @pytest.mark.parametrize("B", [40, 5000])
