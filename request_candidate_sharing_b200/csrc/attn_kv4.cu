@@ -18,7 +18,8 @@
 // warp streams its own 64-key chunks through a ring of bulk copies and keeps its own running
 // maximum, sum and output, joined through shared memory at the end, so the loop has no block-wide
 // wait.  Short histories of many requests give each warp a head of its own instead.  Where the (tile, head) items are too few to fill the GPU the keys are split over blocks,
-// whose partial results a second launch joins in a fixed order.
+// whose partial results another launch joins in a fixed order; where they are more than it holds, a list
+// made on the device starts the longest first.
 #include <float.h>
 
 #include <type_traits>
@@ -92,17 +93,14 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3;
   // p.per_item warps (1, 2 or 4) share a (tile, head); the block has 4 / per_item neighbouring heads
   const int heads = KA_WARPS / p.per_item, part = warp & (p.per_item - 1);
-  const int h = blockIdx.y * heads + warp / p.per_item;
-
-  if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
   KaTile a;
-  if (!ka_tile(p, blockIdx.x, T, a)) return;
+  int c_lo, c_hi, place, group;
+  if (!ka_work(p, T, C::KEYS_LOG2, a, c_lo, c_hi, place, group)) return;
+  const int h = group * heads + warp / p.per_item;
   const int last = min(a.first + T, a.n) - 1;       // last packed row of the tile
   const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
   const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
-  const int chunks = h < p.Hkv ? (seen + C::KEYS - 1) / C::KEYS : 0;
-  const int c_lo = (int)((long long)chunks * blockIdx.z / p.n_split);
-  const int c_hi = (int)((long long)chunks * (blockIdx.z + 1) / p.n_split);
+  if (h >= p.Hkv) c_hi = c_lo;
 
   uint8_t* ring = ka_smem + warp * C::RING;
   if (lane == 0)
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   const int live = min(T, a.n - a.first);
   for (int i = threadIdx.x; i < heads * live * (D / 2); i += KA_WARPS * 32) {
     const int d = 2 * (i % (D / 2)), hr = i / (D / 2), hi = hr / live, row = hr - hi * live;
-    const int hh = blockIdx.y * heads + hi, w0 = hi * p.per_item;
+    const int hh = group * heads + hi, w0 = hi * p.per_item;
     if (hh >= p.Hkv) break;
     float top = s_m[w0][row];
     for (int w = 1; w < p.per_item; ++w) top = fmaxf(top, s_m[w0 + w][row]);
@@ -434,12 +432,12 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
       y = fmaf(f, v.y, y);
     }
     const int m = a.first + row;
-    if (p.n_split == 1) {
+    if (place < 0) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;      // a row that sees nothing is zero
       __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)hh * p.share + m % p.share) * D + d;
       *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
     } else {
-      const long long at = ((((long long)blockIdx.x * p.Hkv + hh) * p.n_split + blockIdx.z) * T + row);
+      const long long at = ((long long)place * p.Hkv + hh) * T + row;
       *reinterpret_cast<float2*>(p.part + at * D + d) = make_float2(x, y);
       if (d == 0) p.part_ml[at] = make_float2(top, l);
     }
@@ -454,30 +452,29 @@ template <int D, int T>
 __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, int rows_per_block) {
   constexpr int GROUPS = 256 / D;
   __shared__ float s_part[GROUPS][D + 2];
-  KaTile a;
-  // (offsets and lengths are the caller's, not the launch's before this one)
-  const bool has = ka_tile(p, blockIdx.x, T, a);
   grid_dependency_wait();
-  if (!has) return;
+  if ((int)blockIdx.x >= p.counts[1]) return;
+  const KaJoin a = p.joins[blockIdx.x];
+  const int n = a.n_r * p.share;
   const int h = blockIdx.y, grp = threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
-  const bool shared_row = p.n_split > KJ_SPLITS;
+  const bool shared_row = a.parts > KJ_SPLITS;
   const int row_step = shared_row ? 1 : GROUPS, split_step = shared_row ? GROUPS : 1;
-  const long long item0 = ((long long)blockIdx.x * p.Hkv + h) * p.n_split;
-  const int row_end = min((int)(blockIdx.z + 1) * rows_per_block, a.n - a.first);
+  const long long stride = (long long)p.Hkv * T, at0 = (long long)a.part * stride + h * T;     // of the parts' rows
+  const int row_end = min((int)(blockIdx.z + 1) * rows_per_block, n - a.first);
   for (int row0 = blockIdx.z * rows_per_block; row0 < row_end; row0 += row_step) {
     const int row = row0 + (shared_row ? 0 : grp);
     float top = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
     if (row < row_end) {
-      for (int s0 = shared_row ? grp : 0; s0 < p.n_split; s0 += 4 * split_step) {
+      for (int s0 = shared_row ? grp : 0; s0 < a.parts; s0 += 4 * split_step) {
         float2 ml[4], v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int sp = s0 + i * split_step;
           ml[i] = make_float2(-INFINITY, 0.f);
           v[i] = make_float2(0.f, 0.f);
-          if (sp < p.n_split) {
-            ml[i] = p.part_ml[(item0 + sp) * T + row];
-            v[i] = *reinterpret_cast<const float2*>(p.part + ((item0 + sp) * T + row) * D + d);
+          if (sp < a.parts) {
+            ml[i] = p.part_ml[at0 + sp * stride + row];
+            v[i] = *reinterpret_cast<const float2*>(p.part + (at0 + sp * stride + row) * D + d);
           }
         }
         float m = top;
@@ -522,58 +519,219 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, in
     if (row < row_end && (!shared_row || grp == 0)) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int m = a.first + row;
-      __nv_bfloat16* out = p.O + (a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
+      __nv_bfloat16* out = p.O + ((long long)a.q0 + m / p.share) * p.ldo + ((long long)h * p.share + m % p.share) * D + d;
       *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(x * inv, y * inv);
     }
   }
 }
 
-// How a call is laid out: rows per tile, an upper bound of its tiles, and the key splits.
+// The list of blocks' work, by one block, up to KL_MAX requests.  Tiles come in the order of their key
+// units, most first (a counting sort; the order of equal ones does not matter to any result): a request's
+// blocks take as long as its keys are many, and started last they would leave most of the GPU idle.
+// Where tiles are few, their keys are split so that each block gets about 1.1 times the mean of a
+// block per slot, but no less than min_units.
+// One block's straight run through code that nothing has run before it is mostly instruction fetches, so
+// the code is short: loops are not unrolled, and a request is read again (from L1) in each of the passes.
+constexpr int KL_THREADS = 512, KL_MAX = 8192, KL_OWN = 8;
+struct KaListParams {
+  int T, unit_log2, split, slots, min_units, weight_shift;
+};
+struct KlReq {
+  int q0, n_r, len, tiles, units;
+};
+__device__ __forceinline__ KlReq kl_request(const KaParams& p, const KaListParams& l, int r, bool tell) {
+  KlReq q = {0, 0, 0, 0, 0};
+  const int a = p.offsets[r], b = p.offsets[r + 1], len = p.kv_len[r];
+  if (a < 0 || b < a || b > p.rows) {
+    if (tell) set_status(p.status, ROCS_ERR_INDEX);
+  } else if (len < 0 || len > ((long long)p.max_blocks << p.P_log2)) {
+    if (tell) set_status(p.status, ROCS_ERR_COUNTS);
+  } else {
+    q.q0 = a;
+    q.n_r = b - a;
+    q.len = len;
+    q.tiles = ((b - a) * p.share + l.T - 1) / l.T;
+    q.units = (len + (1 << l.unit_log2) - 1) >> l.unit_log2;
+  }
+  return q;
+}
+
+__global__ void __launch_bounds__(KL_THREADS) ka_list_kernel(const KaParams p, const KaListParams l) {
+  __shared__ unsigned s_at[KL_THREADS], s_warp[KL_THREADS / 32];
+  __shared__ unsigned long long s_units;
+  __shared__ int s_joins, s_parts;
+  grid_dependents_launch();
+  const int tid = threadIdx.x, lane = tid & 31;
+  s_at[tid] = 0;
+  if (tid == 0) {
+    s_units = 0;
+    s_joins = s_parts = 0;
+  }
+  __syncthreads();
+  int most = 1 << 30;
+  if (l.split) {
+    unsigned long long sum = 0;
+#pragma unroll 1
+    for (int r = tid; r < p.B_R; r += KL_THREADS) {
+      const KlReq q = kl_request(p, l, r, false);
+      sum += (unsigned long long)q.tiles * q.units * p.groups;
+    }
+    if (sum > 0) atomicAdd(&s_units, sum);
+    __syncthreads();
+    const unsigned mean = (unsigned)(s_units / (unsigned)l.slots);      // (far below 2^32: see ka_plan)
+    most = max(l.min_units, (int)(mean + mean / 10 + 1));
+  }
+  // the bucket of a request's blocks, by their key units, most first
+  auto bucket = [&](int units, int splits) {
+    return KL_THREADS - 1 - min((units + splits - 1) / splits >> l.weight_shift, KL_THREADS - 1);
+  };
+#pragma unroll 1
+  for (int r = tid; r < p.B_R; r += KL_THREADS) {
+    const KlReq q = kl_request(p, l, r, true);
+    const int splits = q.units > most ? (q.units + most - 1) / most : 1;
+    if (q.tiles > 0) atomicAdd(&s_at[bucket(q.units, splits)], (unsigned)(q.tiles * splits));
+  }
+  __syncthreads();
+  // exclusive running total over the buckets
+  const unsigned v = s_at[tid];
+  unsigned incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_warp[tid >> 5] = incl;
+  __syncthreads();
+  unsigned before = 0;
+#pragma unroll 1
+  for (int w = 0; w < (tid >> 5); ++w) before += s_warp[w];
+  s_at[tid] = before + incl - v;
+  if (tid == KL_THREADS - 1) p.counts[0] = (int)(before + incl);
+  __syncthreads();
+#pragma unroll 1
+  for (int r0 = tid - lane; r0 < p.B_R; r0 += KL_THREADS) {
+    const int r = r0 + lane;
+    KlReq q = {0, 0, 0, 0, 0};
+    if (r < p.B_R) q = kl_request(p, l, r, false);
+    const int splits = q.units > most ? (q.units + most - 1) / most : 1, n = q.tiles * splits;
+    unsigned at = 0;
+    int part = 0, join = 0;
+    if (n > 0) {
+      at = atomicAdd(&s_at[bucket(q.units, splits)], (unsigned)n);
+      if (splits > 1) {
+        part = atomicAdd(&s_parts, n);
+        join = atomicAdd(&s_joins, q.tiles);
+      }
+    }
+    // a request's entries by its own thread, or by the warp where they are many
+    const uint32_t many = __ballot_sync(0xffffffffu, n > KL_OWN);
+    const int turns = 1 + __popc(many);
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn) {
+      const int w = turn == 0 ? lane : (int)__fns(many, 0, turn);
+      KlReq x;
+      x.q0 = __shfl_sync(0xffffffffu, q.q0, w);
+      x.n_r = __shfl_sync(0xffffffffu, q.n_r, w);
+      x.len = __shfl_sync(0xffffffffu, q.len, w);
+      const int sp = __shfl_sync(0xffffffffu, splits, w), xn = __shfl_sync(0xffffffffu, n, w);
+      const int xp = __shfl_sync(0xffffffffu, part, w), xj = __shfl_sync(0xffffffffu, join, w);
+      const unsigned xa = __shfl_sync(0xffffffffu, at, w);
+      const int end = turn == 0 && xn > KL_OWN ? 0 : xn, step = turn == 0 ? 1 : 32;
+#pragma unroll 1
+      for (int i = turn == 0 ? 0 : lane; i < end; i += step) {
+        const int t = i / sp, s = i - t * sp, first = t * l.T;
+        const int last = min(first + l.T, x.n_r * p.share) - 1;
+        const int seen = p.causal ? max(0, x.len - x.n_r + last / p.share + 1) : x.len;
+        const int chunks = (seen + (1 << l.unit_log2) - 1) >> l.unit_log2, each = chunks / sp, more = chunks - each * sp;
+        int4* to = reinterpret_cast<int4*>(&p.items[xa + i]);
+        const int c_lo = each * s + min(s, more);
+        to[0] = make_int4(r0 + w, first, x.n_r, x.len);
+        to[1] = make_int4(x.q0, c_lo, c_lo + each + (s < more ? 1 : 0), sp > 1 ? xp + i : -1);
+        if (sp > 1 && s == 0) p.joins[xj + t] = KaJoin{first, x.n_r, x.q0, xp + i, sp, {0, 0, 0}};
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) p.counts[1] = s_joins;
+}
+
+// How a call is laid out: rows per tile, upper bounds of its tiles and blocks, whether the work is listed
+// and the keys may be split.
 struct KaPlan {
-  int NT = 1, T = 8, n_split = 1;   // NT = 0: the tcgen05 kernel
+  int NT = 1, T = 8;                // NT = 0: the tcgen05 kernel
   int per_item = KA_WARPS;          // warps a (tile, head)
-  long long tiles = 0;
-  size_t part_bytes = 0, bytes = 0;
+  int groups = 1;                   // blocks a tile
+  bool list = false, split = false;
+  int slots = 0;                    // blocks that the GPU holds at once
+  long long tiles = 0;              // without a list; with one, the list's length at most
+  long long joins = 0, parts = 0;
+  size_t items_at = 0, joins_at = 0, part_at = 0, ml_at = 0, bytes = 0;
 };
 
 KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R, long long rows, int max_blocks) {
   KaPlan k;
+  if (rows == 0) return k;
   const int share = H_q / d.H_kv;
   const long long packed = rows * share;
   // as many packed rows per tile as a request has on average
   const double avg = (double)packed / B_R;
-    k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
+  k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
   k.T = k.NT > 0 ? 8 * k.NT : 128;
-  k.tiles = packed / k.T + B_R;
   // about as many tiles as will have rows: a request's rows begin a tile of their own
   const long long full = packed / k.T, own = rows < B_R ? rows : B_R;
   const long long busy = full > own ? full : own;
   const long long items = (busy < 1 ? 1 : busy) * d.H_kv;
-  // the keys are split until the blocks fill the GPU once (three an SM with d = 128, else four; two or
-  // three of the 128-row kernel's), not beyond: a second, partly filled wave costs more
-  const long long slots = (k.NT > 0 ? (d.d_h == 128 ? 3LL : 4LL) : d.d_h == 32 ? 3LL : 2LL) * ctx->num_sms;
-  const long long longest = ((long long)max_blocks * d.page_size + 63) / 64;
-  long long split = slots / items;
-  const long long most = longest / (k.NT > 0 ? 4 * KA_WARPS : 8);
-  split = split > most ? most : split;
-  k.n_split = (int)(split < 1 ? 1 : split > 1024 ? 1024 : split);
   // one warp an item where items fill the GPU's warps (16 an SM) more than once, two where they nearly do:
   // 41 instead of 57 us on 4096 items of 500 keys (d = 32), 42 instead of 46 us on 1200 with four warps (d = 64)
-  k.per_item = items >= 24LL * ctx->num_sms ? 1 : items >= 12LL * ctx->num_sms ? 2 : 4;
-  if (k.n_split > 1) {
-    const size_t n = (size_t)k.tiles * d.H_kv * k.n_split * k.T;
-    k.part_bytes = (n * d.d_h * 4 + 255) / 256 * 256;
-    k.bytes = k.part_bytes + n * 8;
+  if (k.NT > 0) k.per_item = items >= 24LL * ctx->num_sms ? 1 : items >= 12LL * ctx->num_sms ? 2 : 4;
+  const int heads = k.NT > 0 ? KA_WARPS / k.per_item : 1;
+  k.groups = (d.H_kv + heads - 1) / heads;
+  const int an_sm = k.NT == 0 ? (d.d_h == 32 ? 3 : 2) : k.NT > 1 ? 2 : d.d_h == 32 ? 5 : d.d_h == 64 ? 4 : 3;
+  k.slots = an_sm * ctx->num_sms;
+  const long long blocks = (busy < 1 ? 1 : busy) * k.groups;
+  const long long longest = (long long)max_blocks * d.page_size;
+  k.split = blocks <= k.slots / 2 && longest >= (k.NT > 0 ? 2048 : 1024) && B_R <= KL_MAX;
+  // the list costs a launch of its own (3 us): where blocks outnumber the slots, for its order; where they
+  // are few, for the splits; and always in front of the tcgen05 kernel, whose set-up hides it
+  k.list = B_R <= KL_MAX && (k.split || k.NT == 0 || blocks > k.slots);
+  k.tiles = packed / k.T + B_R;
+  if (k.list) {
+    if (k.tiles > packed) k.tiles = packed;
+    // with u units in all and m = 1.1 u / slots a block, a tile of x units becomes ceil(x / m) <= 1 + x / m
+    // blocks, and one with x > m at most 2 x / m
+    k.joins = k.split ? k.tiles : 0;
+    k.parts = k.split ? 2LL * k.slots / k.groups + 2 : 0;
+    if (k.split) k.tiles += k.slots / k.groups + 1;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    k.items_at = 256;
+    k.joins_at = up(k.items_at + (size_t)k.tiles * sizeof(KaItem));
+    k.part_at = up(k.joins_at + (size_t)k.joins * sizeof(KaJoin));
+    k.ml_at = up(k.part_at + (size_t)k.parts * d.H_kv * k.T * d.d_h * 4);
+    k.bytes = k.ml_at + (size_t)k.parts * d.H_kv * k.T * 8;
   }
   return k;
+}
+
+rocs_status ka_list(const KaParams& p, const KaPlan& k, int unit_log2, cudaStream_t s) {
+  KaListParams l;
+  l.T = k.T;
+  l.unit_log2 = unit_log2;
+  l.split = k.split ? 1 : 0;
+  l.slots = k.slots;
+  l.min_units = (k.NT > 0 ? 1024 : 512) >> unit_log2;
+  l.weight_shift = 0;
+  while ((((long long)p.max_blocks << p.P_log2) >> unit_log2 >> l.weight_shift) >= KL_THREADS) ++l.weight_shift;
+  LaunchTimer lt_("attn_kv4_list", s);
+  ka_list_kernel<<<1, KL_THREADS, 0, s>>>(p, l);
+  return cuda_check(cudaGetLastError(), "ka_list_kernel");
 }
 
 template <int D, int T>
 rocs_status ka_join(const KaParams& p, const KaPlan& k, cudaStream_t s) {
   LaunchTimer lt_("attn_kv4_join", s);
-  // a block takes one row of many splits, or 16 rows of a few
-  const int rows = k.n_split > KJ_SPLITS ? 1 : T < 16 ? T : 16;
-  return launch_dependent(attn_kv4_join_kernel<D, T>, dim3((unsigned)k.tiles, p.Hkv, T / rows), dim3(128), 0, s, "attn_kv4_join_kernel",
+  // a block takes one row, or 16 of a 128-row tile
+  const int rows = T < 128 ? 1 : 16;
+  return launch_dependent(attn_kv4_join_kernel<D, T>, dim3((unsigned)k.joins, p.Hkv, T / rows), dim3(128), 0, s, "attn_kv4_join_kernel",
                           p, rows);
 }
 
@@ -588,14 +746,18 @@ rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cud
     if (st != ROCS_OK) return st;
     if (ctx->device < 64) attr[ctx->device] = true;
   }
+  rocs_status st;
   {
     LaunchTimer lt_("attn_kv4", s);
-    const int heads = KA_WARPS / k.per_item;
-    attn_kv4_kernel<D, NT, BIG>
-        <<<dim3((unsigned)k.tiles, (p.Hkv + heads - 1) / heads, k.n_split), KA_WARPS * 32, C::SMEM, s>>>(p);
+    const dim3 grid((unsigned)(k.tiles * k.groups)), block(KA_WARPS * 32);
+    if (k.list) {
+      st = launch_dependent(attn_kv4_kernel<D, NT, BIG>, grid, block, C::SMEM, s, "attn_kv4_kernel", p);
+    } else {
+      attn_kv4_kernel<D, NT, BIG><<<grid, block, C::SMEM, s>>>(p);
+      st = cuda_check(cudaGetLastError(), "attn_kv4_kernel");
+    }
   }
-  rocs_status st = cuda_check(cudaGetLastError(), "attn_kv4_kernel");
-  return st != ROCS_OK || k.n_split == 1 ? st : ka_join<D, 8 * NT>(p, k, s);
+  return st != ROCS_OK || !k.split ? st : ka_join<D, 8 * NT>(p, k, s);
 }
 
 template <int D, int NT>
@@ -605,9 +767,13 @@ rocs_status ka_launch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cud
 
 template <int D>
 rocs_status ka_dispatch(rocs_context* ctx, const KaParams& p, const KaPlan& k, cudaStream_t s) {
+  if (k.list) {
+    rocs_status st = ka_list(p, k, k.NT == 0 ? 6 : KaCfg<D>::KEYS_LOG2, s);
+    if (st != ROCS_OK) return st;
+  }
   if (k.NT == 0) {
-    rocs_status st = launch_attn_kv4_tc(ctx, D, p, k.tiles, s);
-    if (st != ROCS_OK || k.n_split == 1) return st;
+    rocs_status st = launch_attn_kv4_tc(ctx, D, p, k.tiles * k.groups, s);
+    if (st != ROCS_OK || !k.split) return st;
     return ka_join<D, 128>(p, k, s);
   }
   if (k.NT == 1) return ka_launch<D, 1>(ctx, p, k, s);
@@ -628,6 +794,10 @@ rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const voi
                             long long ldo, void* scratch, cudaStream_t s) {
   if (rows == 0) return ROCS_OK;
   const KaPlan k = ka_plan(ctx, d, H_q, B_R, rows, max_blocks);
+  if (k.tiles * k.groups > 2147483647LL) {
+    set_error("rocs_dca_cross_attn_kv4: B_R=%d requests of %d heads are too many blocks", B_R, d.H_kv);
+    return ROCS_ERR_INVALID_ARG;
+  }
   KaParams p;
   p.Q = (const __nv_bfloat16*)Q;
   p.ldq = ldq;
@@ -648,10 +818,14 @@ rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const voi
   p.causal = causal;
   p.O = (__nv_bfloat16*)O;
   p.ldo = ldo;
-  p.n_split = k.n_split;
   p.per_item = k.per_item;
-  p.part = (float*)scratch;
-  p.part_ml = (float2*)((char*)scratch + k.part_bytes);
+  p.groups = k.groups;
+  char* ws = (char*)scratch;
+  p.counts = k.list ? (int*)ws : nullptr;
+  p.items = k.list ? (KaItem*)(ws + k.items_at) : nullptr;
+  p.joins = k.list ? (KaJoin*)(ws + k.joins_at) : nullptr;
+  p.part = k.list ? (float*)(ws + k.part_at) : nullptr;
+  p.part_ml = k.list ? (float2*)(ws + k.ml_at) : nullptr;
   p.status = ctx->d_status;
   switch (d.d_h) {
     case 32: return ka_dispatch<32>(ctx, p, k, s);

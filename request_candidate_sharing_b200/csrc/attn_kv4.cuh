@@ -9,6 +9,19 @@
 
 namespace rocs {
 
+// A block's work: tile `first` .. (packed rows) of request r, whose n_r query rows begin at q0 and whose
+// keys are len; key units [c_lo, c_hi) of `unit` keys; the partial result's place, or -1 where the block
+// has all of the tile's keys and writes its output.
+struct __align__(16) KaItem {
+  int r, first, n_r, len;
+  int q0, c_lo, c_hi, part;
+};
+// A tile whose keys were split: its `parts` partial results from `part` on.
+struct __align__(16) KaJoin {
+  int first, n_r, q0, part;
+  int parts, pad[3];
+};
+
 struct KaParams {
   const __nv_bfloat16* Q;
   long long ldq;
@@ -24,9 +37,14 @@ struct KaParams {
   int causal;
   __nv_bfloat16* O;
   long long ldo;
-  int n_split;
   int per_item;         // warps a (tile, head) of the kernel for few rows
-  float* part;          // [tile][head][split][row][D] sums, then [tile][head][split][row] (max, sum) pairs
+  int groups;           // blocks a tile: its heads, or groups of them
+  // the list of blocks' work, heaviest first, made by ka_list_kernel; null: block = tile * groups + group,
+  // in the order of the requests
+  int* counts;          // items, joins
+  KaItem* items;
+  KaJoin* joins;
+  float* part;          // [part][head][row][D] sums, and [part][head][row] (max, sum) pairs
   float2* part_ml;
   int* status;
 };
@@ -54,10 +72,10 @@ __device__ __forceinline__ int ka_request(const KaParams& p, long long t, int T)
   return lo;
 }
 
-// Every request's lengths are looked at once, whether a tile reads them or not; the grid's x extent is
-// at least B_R.
+// Every request's lengths are looked at once, whether a tile reads them or not, by the blocks that work
+// without a list (there are at least B_R of them, and each looks at 32).
 __device__ __forceinline__ void ka_check_lengths(const KaParams& p) {
-  const long long r = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long r = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
   if (r >= p.B_R) return;
   const long long q0 = p.offsets[r], q1 = p.offsets[r + 1], len = p.kv_len[r];
   if (q0 < 0 || q1 < q0 || q1 > p.rows) set_status(p.status, ROCS_ERR_INDEX);
@@ -85,51 +103,34 @@ __device__ __forceinline__ bool ka_tile(const KaParams& p, long long t, int T, K
   return true;
 }
 
-// The same for a whole block of 256 threads, in one round of loads up to 1024 requests (the start of a
-// tile is a chain of latencies: 3300 cycles with the warp's search, of some 20000 a tile): each
-// thread looks at up to four requests, and whoever finds the tile's publishes all there is to it.
-__device__ __forceinline__ bool ka_tile_block(const KaParams& p, long long t, int T, KaTile& a) {
-  __shared__ KaTile s_tile;
-  __shared__ int s_found;
-  if (p.B_R > 1024) return ka_tile(p, t, T, a);
-  if (threadIdx.x == 0) s_found = 0;
-  long long o[5];
-  int len[4];
-  const int r0 = threadIdx.x * 4;
-#pragma unroll
-  for (int i = 0; i < 5; ++i) o[i] = r0 + i <= p.B_R ? p.offsets[r0 + i] : -1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) len[i] = r0 + i < p.B_R ? p.kv_len[r0 + i] : -1;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i;
-    if (r >= p.B_R || o[i] < 0 || o[i + 1] < o[i] || o[i + 1] > p.rows || len[i] < 0 ||
-        len[i] > ((long long)p.max_blocks << p.P_log2))
-      continue;
-    const long long ti = t - (o[i] * p.share / T + r), n = (o[i + 1] - o[i]) * p.share;
-    if (ti < 0 || ti * T >= n) continue;
-    // with offsets in order no other request has this tile; otherwise any of them will do
-    if (atomicExch(&s_found, 1) == 0) {
-      s_tile.r = r;
-      s_tile.q0 = o[i];
-      s_tile.n_r = (int)(o[i + 1] - o[i]);
-      s_tile.n = (int)n;
-      s_tile.first = (int)(ti * T);
-      s_tile.len = len[i];
-    }
-  }
-  __syncthreads();
-  a = s_tile;
-  return s_found != 0;
-}
-
 // Keys that packed row m of the tile's request sees: [0, limit).
 __device__ __forceinline__ int ka_limit(const KaParams& p, const KaTile& a, int m) {
   return p.causal ? max(0, a.len - a.n_r + m / p.share + 1) : a.len;
 }
 
-// Many query rows per request (attn_kv4_tc.cu): tiles of 128 packed rows, p.n_split splits of the keys.
-rocs_status launch_attn_kv4_tc(rocs_context* ctx, int d_h, const KaParams& p, long long tiles, cudaStream_t s);
+// What this block does: its tile, its key units and its partial's place (-1: none), and its head or group of
+// heads; false where there is nothing to do.  For a whole warp.
+__device__ __forceinline__ bool ka_work(const KaParams& p, int T, int unit_log2, KaTile& a, int& c_lo, int& c_hi, int& part, int& group) {
+  const unsigned b = blockIdx.x, t = b / (unsigned)p.groups;
+  group = (int)(b - t * (unsigned)p.groups);
+  if (p.items != nullptr) {
+    grid_dependency_wait();
+    if ((int)t >= p.counts[0]) return false;
+    const int4 x = *reinterpret_cast<const int4*>(&p.items[t]), y = *(reinterpret_cast<const int4*>(&p.items[t]) + 1);
+    a.r = x.x; a.first = x.y; a.n_r = x.z; a.len = x.w;
+    a.q0 = y.x; c_lo = y.y; c_hi = y.z; part = y.w;
+    a.n = a.n_r * p.share;
+    return true;
+  }
+  ka_check_lengths(p);
+  if (!ka_tile(p, t, T, a)) return false;
+  c_lo = 0;
+  c_hi = (ka_limit(p, a, min(a.first + T, a.n) - 1) + (1 << unit_log2) - 1) >> unit_log2;
+  part = -1;
+  return true;
+}
+
+// Many query rows per request (attn_kv4_tc.cu): tiles of 128 packed rows, units of 64 keys.
+rocs_status launch_attn_kv4_tc(rocs_context* ctx, int d_h, const KaParams& p, long long blocks, cudaStream_t s);
 
 }  // namespace rocs

@@ -102,23 +102,13 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
   __shared__ uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], q_full, s_full[2], p_full[2], pv_done[2], drain;
   __shared__ uint32_t s_bad[8];            // per block (mod 8): 16-key pieces whose page does not exist
   __shared__ uint32_t tmem_slot[2];
+  __shared__ KaTile s_tile;
+  __shared__ int4 s_range;                 // first block, blocks, partial's place, head
   __shared__ volatile int abort_flag;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kt_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
   uint8_t* sKV = base + C::Q_BYTES;        // [STAGES][K | V]
   const int warp = threadIdx.x >> 5;
-  const int h = blockIdx.y;
-
-  if (blockIdx.y == 0 && blockIdx.z == 0) ka_check_lengths(p);
-  KaTile a;
-  if (!ka_tile_block(p, blockIdx.x, KT_ROWS, a)) return;
-  const int last = min(a.first + KT_ROWS, a.n) - 1;
-  const int seen = ka_limit(p, a, last);            // keys that any row of the tile sees
-  const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
-  const int blocks = (seen + KT_KEYS - 1) / KT_KEYS;
-  const int b_lo = (int)((long long)blocks * blockIdx.z / p.n_split);
-  const int n = (int)((long long)blocks * (blockIdx.z + 1) / p.n_split) - b_lo;
-
   if (threadIdx.x < 8) s_bad[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -140,11 +130,25 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
     if (C::MORE_COLS > 0) tmem_alloc(&tmem_slot[1], C::MORE_COLS);
     tmem_relinquish();
   }
+  // looked up while thread 0 and warp 7 set up (with a list it may still be in the making); without any work
+  // every role has zero blocks and nothing is written
+  if (warp == 4) {
+    KaTile w;
+    int lo = 0, hi = 0, place = -1, group = 0;
+    if (!ka_work(p, KT_ROWS, 6, w, lo, hi, place, group)) {
+      w = KaTile{};
+      hi = lo;
+    }
+    s_tile = w;
+    s_range = make_int4(lo, hi - lo, place, group);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const KaTile a = s_tile;
+  const int b_lo = s_range.x, n = s_range.y, part = s_range.z, h = s_range.w;
+  const int sees_all = ka_limit(p, a, a.first);     // keys that every row sees
   const uint32_t s_tmem = tmem_slot[0], o_tmem = C::MORE_COLS > 0 ? tmem_slot[1] : s_tmem + 2 * KT_KEYS;
-
   if (warp < 4) {
     // ---------------- softmax: thread = row = TMEM lane ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX));
@@ -251,8 +255,8 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, &abort_flag));
     if (ok && warp_live) {
       tc_fence_after();
-      const long long item = (((long long)blockIdx.x * p.Hkv + h) * p.n_split + blockIdx.z) * KT_ROWS + row;
-      const float inv = p.n_split > 1 ? 1.f : l == 0.f ? 0.f : 1.0f / l;    // a row that sees nothing is zero
+      const long long item = ((long long)part * p.Hkv + h) * KT_ROWS + row;
+      const float inv = part >= 0 ? 1.f : l == 0.f ? 0.f : 1.0f / l;    // a row that sees nothing is zero
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t w[16];
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
         float o[16];   // columns back in order
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[(e & 8) + ((e & 7) >> 1) + 4 * (e & 1)] = __uint_as_float(w[e]) * inv;
-        if (live && p.n_split == 1) {
+        if (live && part < 0) {
           __nv_bfloat16* out = p.O + qrow * p.ldo + col + 16 * c;
 #pragma unroll
           for (int e = 0; e < 16; e += 8)
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
           for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(out + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (live && p.n_split > 1) p.part_ml[item] = make_float2(m_cur, l);
+      if (live && part >= 0) p.part_ml[item] = make_float2(m_cur, l);
     }
   } else if (warp != 7) {
     // ---------------- producers ----------------
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
 }
 
 template <int D>
-rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long tiles, cudaStream_t s) {
+rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long blocks, cudaStream_t s) {
   using C = KtCfg<D>;
   static bool attr[64] = {false};
   if (ctx->device >= 64 || !attr[ctx->device]) {
@@ -441,17 +445,19 @@ rocs_status kt_launch(rocs_context* ctx, const KaParams& p, long long tiles, cud
     if (ctx->device < 64) attr[ctx->device] = true;
   }
   LaunchTimer lt_("attn_kv4_tc", s);
-  attn_kv4_tc_kernel<D><<<dim3((unsigned)tiles, p.Hkv, p.n_split), C::THREADS, C::SMEM, s>>>(p);
+  if (p.items != nullptr)
+    return launch_dependent(attn_kv4_tc_kernel<D>, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, s, "attn_kv4_tc_kernel", p);
+  attn_kv4_tc_kernel<D><<<(unsigned)blocks, C::THREADS, C::SMEM, s>>>(p);
   return cuda_check(cudaGetLastError(), "attn_kv4_tc_kernel");
 }
 
 }  // namespace
 
-rocs_status launch_attn_kv4_tc(rocs_context* ctx, int d_h, const KaParams& p, long long tiles, cudaStream_t s) {
+rocs_status launch_attn_kv4_tc(rocs_context* ctx, int d_h, const KaParams& p, long long blocks, cudaStream_t s) {
   switch (d_h) {
-    case 32: return kt_launch<32>(ctx, p, tiles, s);
-    case 64: return kt_launch<64>(ctx, p, tiles, s);
-    default: return kt_launch<128>(ctx, p, tiles, s);
+    case 32: return kt_launch<32>(ctx, p, blocks, s);
+    case 64: return kt_launch<64>(ctx, p, blocks, s);
+    default: return kt_launch<128>(ctx, p, blocks, s);
   }
 }
 

@@ -31,6 +31,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // In a kernel launched by launch_dependent: waits until the launch before it in its stream has completed
 // and its writes are visible.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets such a kernel, if one follows, be set up from here on.
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------------------
 // mbarrier
