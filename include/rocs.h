@@ -363,8 +363,9 @@ rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc
  * rows -1 and sets ROCS_ERR_INDEX.
  * The outputs may not overlap the inputs or one another.
  * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 2048
- * requests), 16-byte aligned.  Limits: 1 <= B_R <= 2^24; 0 <= rows < 2^31 - 1; 0 <= n_free < 2^31 - 1;
- * max_blocks >= 1 with max_blocks * P <= 2^31 - 256; page_size 16, 32, 64 or 128. */
+ * requests), 16-byte aligned, for this call alone until its work is done.  Limits: 1 <= B_R <= 2^24;
+ * 0 <= rows < 2^31 - 1; 0 <= n_free < 2^31 - 1; max_blocks >= 1 with max_blocks * P <= 2^31 - 256;
+ * page_size 16, 32, 64 or 128. */
 rocs_status rocs_kv_block_tables_workspace(rocs_handle_t handle, int32_t B_R, size_t* bytes);
 rocs_status rocs_kv_block_tables(rocs_handle_t handle, const int32_t* past_len, const int32_t* new_len, int32_t B_R,
                                  int32_t page_size, const int32_t* free_pages, int32_t n_free, int32_t n_pages,
@@ -405,7 +406,9 @@ rocs_status rocs_qk_norm_rope(rocs_handle_t handle, const rocs_qk_desc* desc, co
  *     aligned).  slots [rows] int64, device: -1 skips the row (append writes nothing for it, gather
  *     leaves its K and V as they were); another slot outside the cache is skipped and sets
  *     ROCS_ERR_INDEX.  The slots of one append are distinct.
- *   Append: a group with an infinity or a NaN is stored as zeros and sets ROCS_ERR_VALUE. */
+ *   Append: a group with an infinity or a NaN is stored as zeros and sets ROCS_ERR_VALUE.
+ *   What a call writes may not overlap what it reads, nor gather's K its V (slices of one buffer with
+ *   equal strides and other columns do not). */
 rocs_status rocs_kv4_append(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* K, int64_t ld_K,
                             const void* V, int64_t ld_V, const int64_t* slots, int64_t rows, void* cache, void* stream);
 rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* cache, const int64_t* slots,
@@ -422,11 +425,13 @@ rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, con
  *   O [rows, H_q * d_h] bf16, row stride ld_O: softmax(q k^T * scale) v; a row that sees no key is 0.
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights enter the second product as
  * bf16.  Offsets that decrease or leave [0, rows] set ROCS_ERR_INDEX, a kv_len outside its range
- * ROCS_ERR_COUNTS: those requests' rows are not written.  A needed page outside [0, n_pages) sets
- * ROCS_ERR_INDEX; its keys are left out.  Rows behind the last request's are left as they were.
- * workspace: rocs_dca_cross_attn_kv4_workspace bytes (may be 0), 256-byte aligned.  Limits: strides
- * multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256; rows * H_q < 2^31;
- * 1 <= B_R <= 2^24; scale finite. */
+ * ROCS_ERR_COUNTS: those requests' rows are not written (none at all where offsets that go back give the
+ * requests more than `rows` rows together).  A needed page outside [0, n_pages) sets ROCS_ERR_INDEX;
+ * its keys are left out.  Rows behind the last request's are left as they were.
+ * workspace: rocs_dca_cross_attn_kv4_workspace bytes (may be 0), 256-byte aligned, for this call alone until
+ * its work is done: calls that may overlap (other streams, graphs replayed side by side) need one each.
+ * O may not overlap Q or the other inputs.  Limits: strides multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256;
+ * rows * H_q <= 2^31 - 256; 1 <= B_R <= 2^24 with B_R * H_kv < 2^30; scale finite. */
 rocs_status rocs_dca_cross_attn_kv4_workspace(rocs_handle_t handle, const rocs_kv4_desc* desc, int32_t H_q,
                                               int32_t B_R, int64_t rows, int32_t max_blocks, size_t* bytes);
 rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* Q, int64_t ld_Q,

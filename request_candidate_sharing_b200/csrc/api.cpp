@@ -851,8 +851,19 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
+// The same for `rows` rows of wa and of wb bytes, lda and ldb bytes apart.  Two interleaved slices of one
+// buffer share nothing, though their spans do: those are told apart by their columns when the strides agree.
+bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows) {
+  if (rows == 0 || !overlap(a, (size_t)((rows - 1) * lda + wa), b, (size_t)((rows - 1) * ldb + wb))) return false;
+  if (lda != ldb) return true;
+  int64_t at = ((int64_t)((uintptr_t)b - (uintptr_t)a)) % lda;
+  if (at < 0) at += lda;
+  return !(at >= wa && at + wb <= lda);
+}
+
 rocs_status check_kv4_rows(const rocs_kv4_desc* d, const void* K, int64_t ld_K, const void* V, int64_t ld_V,
-                           const int64_t* slots, int64_t rows, const void* cache, const char* who) {
+                           const int64_t* slots, int64_t rows, const void* cache, bool gather,
+                           const char* who) {
   ROCS_TRY(check_kv4_desc(d, who));
   ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL, "%s: rows=%lld out of range", who, (long long)rows);
   ROCS_REQUIRE(cache && (rows == 0 || (K && V && slots)), "%s: NULL argument", who);
@@ -860,6 +871,17 @@ rocs_status check_kv4_rows(const rocs_kv4_desc* d, const void* K, int64_t ld_K, 
   ROCS_REQUIRE(ld_K >= width && ld_V >= width && ld_K % 8 == 0 && ld_V % 8 == 0,
                "%s: row strides must be multiples of 8, at least H_kv * d_h", who);
   ROCS_REQUIRE(aligned16(K) && aligned16(V) && aligned16(cache) && ((uintptr_t)slots & 7) == 0, "%s: misaligned", who);
+  if (rows == 0) return ROCS_OK;
+  const size_t n_k = (size_t)((rows - 1) * ld_K + width) * 2, n_v = (size_t)((rows - 1) * ld_V + width) * 2;
+  const size_t n_c = (size_t)d->n_pages * d->H_kv * ((size_t)d->page_size * d->d_h * 9 / 8);
+  ROCS_REQUIRE(!overlap(K, n_k, cache, n_c) && !overlap(V, n_v, cache, n_c), "%s: the cache overlaps the rows", who);
+  if (gather) {
+    ROCS_REQUIRE(!rows_overlap(K, ld_K * 2, width * 2, V, ld_V * 2, width * 2, rows), "%s: the two outputs overlap", who);
+    ROCS_REQUIRE(!overlap(K, n_k, slots, (size_t)rows * 8) && !overlap(V, n_v, slots, (size_t)rows * 8),
+                 "%s: an output overlaps the slots", who);
+  } else {
+    ROCS_REQUIRE(!overlap(cache, n_c, slots, (size_t)rows * 8), "%s: the cache overlaps the slots", who);
+  }
   return ROCS_OK;
 }
 
@@ -868,7 +890,8 @@ rocs_status check_attn_kv4(const rocs_kv4_desc* d, int32_t H_q, int32_t B_R, int
   ROCS_TRY(check_kv4_desc(d, who));
   ROCS_REQUIRE(H_q >= 1 && H_q % d->H_kv == 0, "%s: H_q=%d must be a multiple of H_kv=%d", who, H_q, d->H_kv);
   ROCS_REQUIRE(B_R >= 1 && B_R <= (1 << 24), "%s: B_R=%d out of range", who, B_R);
-  ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL / H_q, "%s: rows=%lld times H_q out of range", who, (long long)rows);
+  ROCS_REQUIRE(rows >= 0 && rows <= (2147483647LL - 255) / H_q, "%s: rows=%lld times H_q out of range", who, (long long)rows);
+  ROCS_REQUIRE((long long)B_R * d->H_kv < (1LL << 30), "%s: B_R=%d times H_kv out of range", who, B_R);
   ROCS_REQUIRE(max_blocks >= 1 && (long long)max_blocks * d->page_size <= kMaxCachedTokens,
                "%s: max_blocks=%d out of range", who, max_blocks);
   return ROCS_OK;
@@ -961,37 +984,19 @@ extern "C" rocs_status rocs_qk_norm_rope(rocs_handle_t h, const rocs_qk_desc* d,
     ROCS_REQUIRE(s.ld >= width && s.ldo >= width && s.ld * esz % 16 == 0 && s.ldo * esz % 16 == 0,
                  "%s: row strides must be multiples of 16 bytes, at least the heads' width", who);
     ROCS_REQUIRE(aligned16(s.x) && aligned16(s.y) && aligned16(s.g), "%s: misaligned", who);
-    // a side in place reads each unit before it writes it; the other side, or a shifted copy of its
-    // own, might be read after.  Two interleaved slices of one buffer do not overlap, though their
-    // spans do: those are told apart by their columns when the strides agree.
-    if (d->rows == 0) continue;
+    // A side in place reads each unit before it writes it; the other side, or a shifted copy of its
+    // own, might be read after.
     for (int j = 0; j < 2; ++j) {
       const Side& o = sides[j];
       if (o.H == 0 || (i == j && s.x == s.y && s.ld == s.ldo)) continue;
-      const int64_t wj = (int64_t)o.H * d->d_h;
-      const size_t ny = ((size_t)(d->rows - 1) * s.ldo + width) * esz, nx = ((size_t)(d->rows - 1) * o.ld + wj) * esz;
-      if (!overlap(s.y, ny, o.x, nx)) continue;
-      bool apart = false;
-      if (s.ldo == o.ld) {
-        const int64_t period = s.ldo * esz;
-        int64_t at = ((int64_t)((uintptr_t)o.x - (uintptr_t)s.y)) % period;
-        if (at < 0) at += period;
-        apart = at >= width * esz && at + wj * esz <= period;
-      }
-      ROCS_REQUIRE(apart, "%s: an output overlaps an input", who);
+      ROCS_REQUIRE(!rows_overlap(s.y, s.ldo * esz, width * esz, o.x, o.ld * esz, (int64_t)o.H * d->d_h * esz, d->rows),
+                   "%s: an output overlaps an input", who);
     }
   }
-  if (d->H_q > 0 && d->H_k > 0 && d->rows > 0) {
-    const int64_t wq = (int64_t)d->H_q * d->d_h, wk = (int64_t)d->H_k * d->d_h;
-    bool clash = overlap(Q_out, ((size_t)(d->rows - 1) * ld_Qo + wq) * esz, K_out, ((size_t)(d->rows - 1) * ld_Ko + wk) * esz);
-    if (clash && ld_Qo == ld_Ko) {
-      const int64_t period = ld_Qo * esz;
-      int64_t at = ((int64_t)((uintptr_t)K_out - (uintptr_t)Q_out)) % period;
-      if (at < 0) at += period;
-      clash = !(at >= wq * esz && at + wk * esz <= period);
-    }
-    ROCS_REQUIRE(!clash, "%s: the two outputs overlap", who);
-  }
+  ROCS_REQUIRE(d->H_q == 0 || d->H_k == 0 ||
+                   !rows_overlap(Q_out, ld_Qo * esz, (int64_t)d->H_q * d->d_h * esz, K_out, ld_Ko * esz,
+                                 (int64_t)d->H_k * d->d_h * esz, d->rows),
+               "%s: the two outputs overlap", who);
   ROCS_TRY(check_current_device(h, who));
   return launch_qk_norm_rope(h, *d, Q, ld_Q, K, ld_K, gamma_q, gamma_k, cos_sin, positions, Q_out, ld_Qo, K_out,
                              ld_Ko, (cudaStream_t)stream);
@@ -1002,7 +1007,7 @@ extern "C" rocs_status rocs_kv4_append(rocs_handle_t h, const rocs_kv4_desc* d, 
                                        void* stream) {
   CtxGuard ctx_guard_(h);
   ROCS_REQUIRE(h, "rocs_kv4_append: handle is NULL");
-  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, "rocs_kv4_append"));
+  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, false, "rocs_kv4_append"));
   ROCS_TRY(check_current_device(h, "rocs_kv4_append"));
   return launch_kv4_append(h, *d, K, ld_K, V, ld_V, slots, rows, cache, (cudaStream_t)stream);
 }
@@ -1012,7 +1017,7 @@ extern "C" rocs_status rocs_kv4_gather(rocs_handle_t h, const rocs_kv4_desc* d, 
                                        int64_t ld_V, void* stream) {
   CtxGuard ctx_guard_(h);
   ROCS_REQUIRE(h, "rocs_kv4_gather: handle is NULL");
-  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, "rocs_kv4_gather"));
+  ROCS_TRY(check_kv4_rows(d, K, ld_K, V, ld_V, slots, rows, cache, true, "rocs_kv4_gather"));
   ROCS_TRY(check_current_device(h, "rocs_kv4_gather"));
   return launch_kv4_gather(h, *d, cache, slots, rows, K, ld_K, V, ld_V, (cudaStream_t)stream);
 }
@@ -1042,12 +1047,19 @@ extern "C" rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t h, const rocs_kv4_d
   ROCS_REQUIRE(aligned16(Q) && aligned16(O) && aligned16(cache), "%s: misaligned", who);
   ROCS_REQUIRE(std::isfinite(scale), "%s: scale not finite", who);
   ROCS_REQUIRE(causal == 0 || causal == 1, "%s: causal must be 0 or 1", who);
+  ROCS_REQUIRE((((uintptr_t)block_table | (uintptr_t)kv_len | (uintptr_t)offsets) & 3) == 0, "%s: misaligned", who);
+  ROCS_TRY(check_current_device(h, who));
   const size_t need = attn_kv4_scratch(h, *d, H_q, B_R, rows, max_blocks);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255))) {
     set_error("%s: workspace of %zu bytes (256-byte aligned) needed", who, need);
     return ROCS_ERR_WORKSPACE;
   }
-  ROCS_TRY(check_current_device(h, who));
+  const size_t n_o = rows == 0 ? 0 : (size_t)((rows - 1) * ld_O + width) * 2;
+  ROCS_REQUIRE(!rows_overlap(O, ld_O * 2, width * 2, Q, ld_Q * 2, width * 2, rows) &&
+                   !overlap(O, n_o, cache, (size_t)d->n_pages * d->H_kv * ((size_t)d->page_size * d->d_h * 9 / 8)) &&
+                   !overlap(O, n_o, block_table, (size_t)B_R * max_blocks * 4) &&
+                   !overlap(O, n_o, kv_len, (size_t)B_R * 4) && !overlap(O, n_o, offsets, (size_t)(B_R + 1) * 4),
+               "%s: the output overlaps an input", who);
   return launch_attn_kv4(h, *d, Q, ld_Q, H_q, cache, block_table, max_blocks, kv_len, offsets, B_R, rows, scale,
                          causal, O, ld_O, workspace, (cudaStream_t)stream);
 }

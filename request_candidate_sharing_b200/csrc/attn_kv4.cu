@@ -550,21 +550,28 @@ __device__ __forceinline__ KlReq kl_request(const KaParams& p, const KaListParam
     q.q0 = a;
     q.n_r = b - a;
     q.len = len;
-    q.tiles = ((b - a) * p.share + l.T - 1) / l.T;
+    q.tiles = (q.n_r * p.share + l.T - 1) / l.T;
     q.units = (len + (1 << l.unit_log2) - 1) >> l.unit_log2;
   }
   return q;
 }
 
+// The warps' sums first: 64-bit additions to one shared word by every thread took 8 us of a call.
+__device__ __forceinline__ void kl_add(unsigned long long* to, unsigned long long x, int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0 && x > 0) atomicAdd(to, x);
+}
+
 __global__ void __launch_bounds__(KL_THREADS) ka_list_kernel(const KaParams p, const KaListParams l) {
   __shared__ unsigned s_at[KL_THREADS], s_warp[KL_THREADS / 32];
-  __shared__ unsigned long long s_units;
+  __shared__ unsigned long long s_units, s_rows;
   __shared__ int s_joins, s_parts;
   grid_dependents_launch();
   const int tid = threadIdx.x, lane = tid & 31;
   s_at[tid] = 0;
   if (tid == 0) {
-    s_units = 0;
+    s_units = s_rows = 0;
     s_joins = s_parts = 0;
   }
   __syncthreads();
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(KL_THREADS) ka_list_kernel(const KaParams p, c
       const KlReq q = kl_request(p, l, r, false);
       sum += (unsigned long long)q.tiles * q.units * p.groups;
     }
-    if (sum > 0) atomicAdd(&s_units, sum);
+    kl_add(&s_units, sum, lane);
     __syncthreads();
     const unsigned mean = (unsigned)(s_units / (unsigned)l.slots);      // (far below 2^32: see ka_plan)
     most = max(l.min_units, (int)(mean + mean / 10 + 1));
@@ -585,13 +592,22 @@ __global__ void __launch_bounds__(KL_THREADS) ka_list_kernel(const KaParams p, c
   auto bucket = [&](int units, int splits) {
     return KL_THREADS - 1 - min((units + splits - 1) / splits >> l.weight_shift, KL_THREADS - 1);
   };
+  unsigned long long rows = 0;
 #pragma unroll 1
   for (int r = tid; r < p.B_R; r += KL_THREADS) {
     const KlReq q = kl_request(p, l, r, true);
     const int splits = q.units > most ? (q.units + most - 1) / most : 1;
+    rows += q.n_r;
     if (q.tiles > 0) atomicAdd(&s_at[bucket(q.units, splits)], (unsigned)(q.tiles * splits));
   }
+  kl_add(&s_rows, rows, lane);
   __syncthreads();
+  // Offsets that go back and forth give requests more rows than there are, and the list more entries than
+  // it has room for: nothing is done then (the status says so already).
+  if (s_rows > (unsigned long long)p.rows) {
+    if (tid == 0) p.counts[0] = p.counts[1] = 0;
+    return;
+  }
   // exclusive running total over the buckets
   const unsigned v = s_at[tid];
   unsigned incl = v;
@@ -697,8 +713,9 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   k.tiles = packed / k.T + B_R;
   if (k.list) {
     if (k.tiles > packed) k.tiles = packed;
-    // with u units in all and m = 1.1 u / slots a block, a tile of x units becomes ceil(x / m) <= 1 + x / m
-    // blocks, and one with x > m at most 2 x / m
+    // With u units in all and m = 1.1 u / slots a block, a tile of x units becomes ceil(x / m) <= 1 + x / m
+    // blocks, and one with x > m at most 2 x / m.  (Splits are for at most 2 * busy tiles, so u is below
+    // slots * 2^27.)
     k.joins = k.split ? k.tiles : 0;
     k.parts = k.split ? 2LL * k.slots / k.groups + 2 : 0;
     if (k.split) k.tiles += k.slots / k.groups + 1;

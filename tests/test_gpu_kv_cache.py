@@ -443,9 +443,19 @@ def test_attention_bad_lengths_and_offsets(R, counts):
     got = c.run(R, 0.125, 0, offsets=off)
     close(got[:o[3]], want[:o[3]], mag[:o[3]])
     assert (got[o[3]:] == 9).all() and status(R) == 5
-    for off in ([-5, 3, 2, 2 ** 31 - 1, 1], [4, 3, 2, 1, 0]):
+    n = c.rows
+    for off in ([-5, 3, 2, 2 ** 31 - 1, 1], [4, 3, 2, 1, 0], [0, n, 0, n, 0], [0, n, n - 1, n, n]):
         c.run(R, 0.125, 0, offsets=np.array(off))
         assert status(R) == 5
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_attention_offsets_that_go_back_and_forth(R, q):
+    """Thousands of requests that all claim every row: refused on the device, within the workspace."""
+    c = Cached(14, [q] * 300, [40] * 300, 2, 1, 32, 16)
+    off = np.where(np.arange(301) % 2 == 0, 0, c.rows)
+    got = c.run(R, 0.2, 0, offsets=off)
+    assert status(R) == 5 and ((got == 9).all() or not np.isnan(got).any())
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
@@ -467,6 +477,80 @@ def test_attention_missing_pages_are_left_out(R, counts, page):
         w = np.exp(s - s.max(-1, keepdims=True))
         w /= w.sum(-1, keepdims=True)
         close(got[:n, h], w @ v, w @ np.abs(v))
+
+
+@pytest.mark.parametrize("q,d,causal", [(1, 32, 0), (1, 64, 1), (34, 32, 0), (34, 32, 1)])
+def test_attention_more_requests_than_are_listed(R, q, d, causal):
+    """Past 8192 requests the blocks find their tiles themselves, for few rows and for many."""
+    B = 8200
+    g = np.random.default_rng(q)
+    counts = np.full(B, q)
+    counts[g.integers(0, B, 200)] = 0
+    counts[77] += 150
+    lens = g.integers(0, 60 if q == 1 else 20, B)
+    c = Cached(15, counts, lens, 1, 1, d, 16)
+    bad = np.array(c.lens)
+    bad[[5, 8000]] = [-1, c.max_blocks * 16 + 1]
+    got = c.run(R, d ** -0.5, causal, kv_len=bad)
+    assert status(R) == 7
+    want, mag = c.want(d ** -0.5, causal)
+    keep = np.ones(c.rows, bool)
+    for r in (5, 8000):
+        keep[c.offsets[r]:c.offsets[r + 1]] = False
+    close(got[keep], want[keep], mag[keep])
+    assert (got[~keep] == 9).all()
+
+
+@pytest.mark.parametrize("counts,lens,d,share,page", [
+    ([1, 1, 1, 1, 1], [30000, 1, 0, 9000, 4097], 64, 2, 64), ([1] * 700, [(37 * i) % 900 for i in range(700)], 32, 1, 64),
+    ([100, 3, 260, 0, 31], [9000, 4000, 700, 50, 1], 128, 1, 128), ([200, 500, 40, 129], [64, 1000, 333, 2049], 32, 2, 16),
+])
+def test_attention_replayed_from_a_graph(R, counts, lens, d, share, page):
+    """The listed, split and joined forms, replayed with other queries and lengths of the same buffers."""
+    from request_candidate_sharing_b200 import rocs
+    c = Cached(16, counts, lens, 2, share, d, page)
+    Hq, B = 2 * share, len(counts)
+    desc, ld = rocs.Kv4Desc(c.n_pages, page, 2, d), 2 * share * d
+    n = R.rocs_dca_cross_attn_kv4_workspace(desc, Hq, B, c.rows, c.max_blocks)
+    assert n > 0
+    t = dict(q=bf16(c.Q).reshape(c.rows, -1).cuda(), cache=torch.from_numpy(c.cache).cuda(), table=dev_i32(c.table), kv=dev_i32(c.lens),
+             off=dev_i32(c.offsets), out=torch.zeros(c.rows, ld, dtype=torch.bfloat16, device="cuda"),
+             ws=torch.full((n,), 255, dtype=torch.uint8, device="cuda"))
+
+    def call(s):
+        R.rocs_dca_cross_attn_kv4(desc, t["q"], ld, Hq, t["cache"], t["table"], c.max_blocks, t["kv"], t["off"], B, c.rows, d ** -0.5, 1, t["out"], ld,
+                                  t["ws"], n, s.cuda_stream)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(side)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call(side)
+            call(side)                      # twice in one graph, with one workspace: in order
+        rng = np.random.default_rng(1)
+        for step in range(3):
+            if step:
+                c.lens = np.array([rng.integers(0, x + 1) for x in lens])
+                c.Q = bf16(rng.normal(size=c.Q.shape)).double().numpy()
+                t["kv"].copy_(dev_i32(c.lens))
+                t["q"].copy_(bf16(c.Q).reshape(c.rows, -1).cuda())
+            t["out"].fill_(9.0)
+            g.replay()
+            side.synchronize()
+            assert R.rocs_get_device_status(side.cuda_stream) == 0
+            close(host(t["out"]).reshape(c.rows, Hq, d), *c.want(d ** -0.5, 1))
+    del g
+
+
+@pytest.mark.parametrize("counts,lens", [([1], [60000]), ([3, 1], [9000, 20000]), ([200], [5000])])
+def test_attention_same_bits_every_time(R, counts, lens):
+    """Lists and partial results are laid out by atomics; the results do not depend on their order."""
+    c = Cached(17, counts, lens, 4, 1, 64, 64)
+    first = c.run(R, 0.125, 0)
+    for _ in range(5):
+        assert np.array_equal(c.run(R, 0.125, 0), first)
 
 
 def test_attention_no_rows(R):
@@ -631,6 +715,53 @@ def test_calls_refuse_another_current_device_or_small_workspace(R):
         with pytest.raises(rocs.RocsError) as e:
             R.rocs_dca_cross_attn_kv4(d, t, 32, 1, t, t, c.max_blocks, t, t, 1, 1, 1.0, 0, t, 32, ws, size, stream())
         assert e.value.status == rocs.ROCS_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("at", [0, 16, 4096 + 512, 9216 + 256, 20480, 24576, 28672])
+def test_attention_refuses_an_output_over_its_inputs(R, at):
+    """Q at 0, the cache at 9216, then the table, the lengths and the offsets."""
+    from request_candidate_sharing_b200 import rocs
+    d = rocs.Kv4Desc(16, 16, 1, 32)            # 9216 bytes
+    t = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    a = t.data_ptr()
+    n = R.rocs_dca_cross_attn_kv4_workspace(d, 8, 1, 10, 1)
+    assert a % 256 == 0 and n <= 32768
+    with pytest.raises(rocs.RocsError) as e:
+        R.rocs_dca_cross_attn_kv4(d, a, 256, 8, a + 9216, a + 20480, 1, a + 24576, a + 28672, 1, 10, 1.0, 0, a + at, 256, a + 32768, n, stream())
+    assert e.value.status == rocs.ROCS_ERR_INVALID_ARG and "overlaps" in str(e.value)
+
+
+def test_attention_output_beside_the_queries_in_one_buffer(R):
+    c = Cached(18, [3, 0, 50], [40, 10, 33], 2, 2, 32, 16)
+    from request_candidate_sharing_b200 import rocs
+    desc = rocs.Kv4Desc(c.n_pages, 16, 2, 32)
+    buf = torch.zeros(c.rows, 256, dtype=torch.bfloat16, device="cuda")
+    buf[:, :128] = bf16(c.Q).reshape(c.rows, -1).cuda()
+    n = R.rocs_dca_cross_attn_kv4_workspace(desc, 4, 3, c.rows, c.max_blocks)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    R.rocs_dca_cross_attn_kv4(desc, buf, 256, 4, torch.from_numpy(c.cache).cuda(), dev_i32(c.table), c.max_blocks, dev_i32(c.lens),
+                              dev_i32(c.offsets), 3, c.rows, 0.2, 0, buf[:, 128:], 256, ws, n, stream())
+    assert status(R) == 0
+    close(host(buf[:, 128:]).reshape(c.rows, 4, 32), *c.want(0.2, 0))
+
+
+def test_calls_refuse_when_another_device_is_current(R):
+    """A handle of another device (only its number is looked at before the refusal)."""
+    import ctypes
+    from request_candidate_sharing_b200 import rocs
+    fake = ctypes.create_string_buffer(256)
+    ctypes.memmove(fake, ctypes.byref(ctypes.c_int32(3)), 4)
+    h = ctypes.cast(fake, ctypes.c_void_p)
+    t = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    a = t.data_ptr()
+    d, q = rocs.Kv4Desc(3, 16, 1, 32), rocs.QkDesc(1, 1, 1, 32, 32, 0, 8, 1e-6, 1)
+    calls = [lambda: rocs._lib_tab(h, a, a + 256, 1, 16, a + 512, 1, 3, a + 1024, 1, a + 1280, a + 1536, a + 2048, a + 2304, 1, a + 2560, None, 0, None),
+             lambda: rocs._lib_qk(h, ctypes.byref(q), a, 32, a + 256, 32, None, None, a + 512, a + 2048, a + 4096, 32, a + 4352, 32, None),
+             lambda: rocs._lib_kv4_app(h, ctypes.byref(d), a, 32, a + 256, 32, a + 512, 1, a + 4096, None),
+             lambda: rocs._lib_kv4_get(h, ctypes.byref(d), a + 4096, a + 512, 1, a, 32, a + 256, 32, None),
+             lambda: rocs._lib_attn4(h, ctypes.byref(d), a, 32, 1, a + 4096, a + 512, 1, a + 768, a + 1024, 1, 1, 1.0, 0, a + 1280, 32, None, 0, None)]
+    for call in calls:
+        assert call() == rocs.ROCS_ERR_INVALID_ARG and "is current" in rocs.rocs_last_error()
 
 
 def test_two_streams_at_once(R):

@@ -235,6 +235,21 @@ def test_kv4_rows_refusals(rocs, h, change):
     assert rocs._lib_kv4_get(h, ctypes.byref(d), a["cache"], a["slots"], a["rows"], a["K"], a["ld_K"], a["V"], a["ld_V"], None) == 1
 
 
+@pytest.mark.parametrize("change,append,gather", [
+    (dict(K=4 << 20), 1, 1), (dict(V=(4 << 20) + 73712), 1, 1), (dict(cache=(1 << 20) + 2544), 1, 1), (dict(slots=(4 << 20) + 64), 1, 0),
+    (dict(V=1 << 20), 0, 1), (dict(V=(1 << 20) + 512), 0, 1), (dict(ld_K=512, V=(1 << 20) + 512, ld_V=504), 0, 1), (dict(slots=(1 << 20) + 80), 0, 1),
+])
+def test_kv4_rows_overlaps_are_refused(rocs, h, change, append, gather):
+    a = {**dict(K=1 << 20, ld_K=256, V=2 << 20, ld_V=256, slots=3 << 20, rows=5, cache=4 << 20), **change}
+    d = rocs.Kv4Desc(4, 64, 8, 32)             # 73728 bytes
+    if append:
+        assert rocs._lib_kv4_app(h, ctypes.byref(d), a["K"], a["ld_K"], a["V"], a["ld_V"], a["slots"], a["rows"], a["cache"], None) == 1
+        assert "overlaps" in rocs.rocs_last_error()
+    if gather:
+        assert rocs._lib_kv4_get(h, ctypes.byref(d), a["cache"], a["slots"], a["rows"], a["K"], a["ld_K"], a["V"], a["ld_V"], None) == 1
+        assert "overlap" in rocs.rocs_last_error()
+
+
 AT = dict(Q=1 << 20, ld_Q=512, H_q=16, cache=2 << 20, table=3 << 20, max_blocks=4, kv=4 << 20, off=5 << 20, B_R=2, rows=7, scale=0.125,
           causal=0, O=6 << 20, ld_O=512, ws=None, ws_bytes=0)
 
@@ -242,9 +257,11 @@ AT = dict(Q=1 << 20, ld_Q=512, H_q=16, cache=2 << 20, table=3 << 20, max_blocks=
 @pytest.mark.parametrize("change", [
     dict(Q=None), dict(cache=None), dict(table=None), dict(kv=None), dict(off=None), dict(O=None), dict(H_q=12), dict(H_q=0), dict(ld_Q=504),
     dict(ld_O=516), dict(Q=(1 << 20) + 8), dict(O=(6 << 20) + 8), dict(cache=(2 << 20) + 8), dict(B_R=0), dict(B_R=1 << 25), dict(rows=-1),
-    dict(rows=1 << 28), dict(max_blocks=0), dict(max_blocks=1 << 25), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2),
+    dict(rows=1 << 28), dict(rows=(2 ** 31 - 255) // 16 + 1), dict(B_R=1 << 24, rows=1, H_q=64, ld_Q=2048, ld_O=2048, H_kv=64), dict(max_blocks=0),
+    dict(kv=(4 << 20) + 2), dict(off=(5 << 20) + 1), dict(table=(3 << 20) + 2),
+    dict(max_blocks=1 << 25), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2),
 ])
 def test_attention_refusals(rocs, h, change):
-    d = rocs.Kv4Desc(40, 64, 8, 32)
-    assert rocs._lib_attn4(h, ctypes.byref(d), *{**AT, **change}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
+    d = rocs.Kv4Desc(40, 64, change.get("H_kv", 8), 32)
+    assert rocs._lib_attn4(h, ctypes.byref(d), *{**AT, **{k: v for k, v in change.items() if k != "H_kv"}}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
     assert "rocs_dca_cross_attn_kv4" in rocs.rocs_last_error()
