@@ -4,21 +4,32 @@
 // One CTA takes 128 packed rows (query row x shared head) of one request against one key head, in
 // blocks of 64 keys; three CTAs share an SM (two with d = 64 or 128), so that one's waits, start and end
 // hide behind the others.
-//   warps 0-3  softmax, one thread per row (TMEM lane): S is read from tensor memory, its maximum
-//              and exponentials are taken in registers, and P
-//              is written back over S as bf16 pairs, the A operand of P V.  The row's reference
-//              maximum moves only when a block exceeds it by more than 2^8.
-//   warps 4-6  (and 8-10 with d = 64 or 128) producers: a thread takes one group (16 bytes of codes and their scale) of a key or a
-//              value at a time, a block ahead in registers, dequantises it (exactly) and writes it as
-//              bf16 into the operand's swizzled tile in shared memory.  The conversion is paid once
-//              per 128 rows; a copy of the codes through shared memory would only lengthen the way.
+//   warps 0-3  softmax, one thread per row (TMEM lane): S is read from tensor memory, its maximum and
+//              exponentials are taken in registers, and P is written back over S as bf16 pairs, the A
+//              operand of P V.  The row's reference maximum moves only when a block exceeds it by more
+//              than 2^8.
+//   warps 4-6  (and 8-10 with d = 64 or 128) producers: a thread takes one group (16 bytes of codes and
+//              their scale) of a key or a value at a time, a block ahead in registers, dequantises it
+//              (exactly) and writes it as bf16 into the operand's swizzled tile in shared memory.  The
+//              conversion is paid once per 128 rows; a copy of the codes through shared memory would only
+//              lengthen the way.
 //   warp 7     issues the MMAs: S_j = Q K_j^T into one of two buffers, O += P_j V_j.  They execute in
 //              order, so S_{j+1} is there when the softmax is done with S_j, and the P in a buffer is
 //              consumed before the S two blocks later lands on it: one wait and one arrival a block.
 // Codes come out of a word as the pairs (0, 4), (1, 5), (2, 6), (3, 7); keys and queries keep that
 // order (a contraction index may be permuted), and the output's columns are put right as they are
-// stored.  Bound by the exponentials; all waits are bounded (ROCS_ERR_DEVICE_TIMEOUT), after which
-// the CTA drains its MMAs, releases tensor memory and returns.
+// stored.  All waits are bounded (ROCS_ERR_DEVICE_TIMEOUT), after which the CTA drains its MMAs, releases
+// tensor memory and returns.
+//
+// Bound by the softmax: the exponential unit is about 61% busy while blocks are full, the rest are the
+// latencies of barriers and tensor memory between its turns.  41388 candidates of 96 requests (8 heads of
+// 32, 675 keys a request on average) take 123 us, of which the exponentials alone are 39 and the products 17;
+// 7601 causal rows of 48 requests (4 heads of 64 shared by two query heads, 2200 keys) 106 us, of 22
+// and 19.
+// Tried and slower there: exponentials by polynomial for 1/8 to 3/8 of the elements (1 to 5%), loads two
+// blocks ahead (145 and 122 us), blocks of 32 keys with four CTAs an SM (124 and 138), three CTAs of one S
+// buffer with d = 64 (146 against 139 then), heads outside tiles in the order of blocks (135 and 133),
+// keys split where blocks are about as many as slots (no gain).
 #include "attn_kv4.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -364,6 +375,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
         }
         fence_proxy_async_smem();
         warp_arrive(&kv_full[st]);
+        // after the fence, which would wait for loads in front of it
         load(j + 1);
         pages(j + 2);
       }

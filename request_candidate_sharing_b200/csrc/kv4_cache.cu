@@ -11,8 +11,7 @@
 //     in the sum's lowest bits, and eight such sums shifted and added are the word of codes plus a
 //     constant.
 //
-// Bound by memory (4 bytes read and 9/8 written per key and value element when appending, the same
-// back) only if an element costs few instructions: an SM has about 14 issue slots' worth of lanes per
+// Bound by memory (2 bytes read and 9/16 written per element when appending, the same back) only if an element costs few instructions: an SM has about 14 issue slots' worth of lanes per
 // element at full bandwidth.  A lane takes eight elements: one 16-byte load, one 4-byte word of codes; a
 // head's row is d / 8 lanes, and a warp takes the keys and values (which share their place in the
 // record) of a few consecutive rows of one head, whose codes lie side by side in a page.  Neighbouring

@@ -8,16 +8,18 @@
 // table already names, so rows and table entries can be written in the same launch.
 //
 // Up to kTabInline requests every block computes both totals by itself in shared memory (two reads of
-// 4 B a request from L2, one block-wide scan): one launch instead of three, and the decode step (512
-// requests, 512 rows) is all launch latency.  Beyond, a block per kTabThreads requests totals its
-// part, a second launch scans and writes the totals, a third expands.  Expansion is by output row, so one request with a million rows spreads over the whole GPU; a warp takes
-// neighbouring rows, and each lane finds its first row's request by binary search in shared memory and
-// walks on (four neighbouring rows a lane, with wide stores, diverged in every warp: 64 us instead of
-// TABBEST for 7.2 M rows).
-// A fresh page's table entry is written by the thread of the page's first row.  Past kTabInline requests
-// a block takes a tile of neighbouring rows, finds its first request by two block-wide probes and brings
-// the requests from there on into shared memory (a search per thread in L2 took most of 90 us for 7.2 M
-// rows of 40000 requests).  Bound by the 12 bytes written per row.
+// 4 B a request from L2, one block-wide scan): one launch instead of three.  A decode step (512 requests,
+// 512 rows) is all latency: with at most four rows a request on average one block does it all without a
+// search, 3.6 us, where the form below takes 9.7 us.
+// Beyond, a block per kTabThreads requests totals its part, a second launch scans and writes the totals,
+// a third expands.  Expansion is by output row, so that one request with a million rows spreads over the
+// whole GPU.  A warp takes neighbouring rows, and each lane finds its first row's request by binary search
+// in shared memory and walks on; a fresh page's table entry is written by the thread of the page's first
+// row.  Past kTabInline requests a block takes a tile of neighbouring rows, finds its first request by two
+// block-wide probes and brings the requests from there on into shared memory.  For 7.2 M rows of 40000
+// requests 44 us: 13.8 us' worth of bytes, the rest latency (two launches of sums, then per tile the
+// probes, the window and the walk's dependent loads of page numbers, one wave).  A search per thread in
+// L2 took 90 us; four neighbouring rows a lane with wide stores, which diverge in every warp, 64 us.
 #include "common.cuh"
 #include "internal.h"
 

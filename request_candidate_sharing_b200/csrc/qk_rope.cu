@@ -10,12 +10,12 @@
 // four whole pairs of a head: with half-split pairs elements 4 l .. 4 l + 3 and their partners d_rot / 2
 // further on, no shuffles; else (neighbouring pairs, or past d_rot) eight neighbours.  A head is d / 8
 // lanes of one warp, the mean a few shuffles, a warp covers 32 / lanes heads of a row at a time; the
-// arithmetic is on packed fp32 pairs, and lanes past d_rot turn by nothing.  A warp
-// takes up to four (row, unit of heads) items of the queries or of the keys, whose elements, positions and then
-// angles it asks for before it works on the first; nothing loops, so that the registers allow many
-// warps.  For 524288 rows of 8 + 8 heads of 32: 201 us (82% of
-// the measured copy bandwidth); 295 us where warps walked over many rows with the
-// next elements in flight, 253 us where each item chose its side.
+// arithmetic is on packed fp32 pairs, and lanes past d_rot turn by nothing.
+// A warp takes up to four (row, unit of heads) items of the queries or of the keys, and asks for their
+// elements, positions and then angles before it works on the first; nothing loops, so that the registers
+// allow many warps.  For 524288 rows of 8 + 8 heads of 32: 201 us (82% of the measured copy bandwidth);
+// 295 us where warps walked over many rows with the next elements in flight, 253 us where each item
+// chose its side.  fp32, 30011 rows of 16 + 2 heads of 128: 91 us (94%).
 #include "common.cuh"
 #include "internal.h"
 
