@@ -13,13 +13,16 @@
 // search, 3.6 us, where the form below takes 9.7 us.
 // Beyond, a block per kTabThreads requests totals its part, a second launch scans and writes the totals,
 // a third expands.  Expansion is by output row, so that one request with a million rows spreads over the
-// whole GPU.  A warp takes neighbouring rows, and each lane finds its first row's request by binary search
-// in shared memory and walks on; a fresh page's table entry is written by the thread of the page's first
-// row.  Past kTabInline requests a block takes a tile of neighbouring rows, finds its first request by two
-// block-wide probes and brings the requests from there on into shared memory.  For 7.2 M rows of 40000
-// requests 44 us: 13.8 us' worth of bytes, the rest latency (two launches of sums, then per tile the
-// probes, the window and the walk's dependent loads of page numbers, one wave).  A search per thread in
-// L2 took 90 us; four neighbouring rows a lane with wide stores, which diverge in every warp, 64 us.
+// whole GPU.  A block takes a tile of neighbouring rows, finds its first request by two block-wide probes,
+// and brings the requests from there on, the pages that their cached tokens end in and the free list's
+// entries of the tile into shared memory, so that nothing waits for memory once rows are written.  A warp
+// goes through its rows request by request; where requests have under 16 rows on average each lane finds
+// its first row's request by binary search and walks on.  For 7.2 M rows of 40000 requests 32 us (5 of
+// them the sums, 3 a tile's start): 13.8 us' worth of bytes.  Page numbers read from L2 as they were needed:
+// 40 us; lanes on their own everywhere: 44 us; a search per row in L2: 90 us; four neighbouring rows a lane
+// with wide stores, which diverge in every warp: 64 us.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,6 +32,7 @@ namespace {
 constexpr int kTabThreads = 512;
 constexpr int kTabItems = 4;                              // requests per thread of a scan
 constexpr int kTabInline = kTabThreads * kTabItems;       // 2048
+constexpr int kTabFree = 2048;                            // entries of the free list that a tile has at hand
 constexpr int kTabRows = 4;                               // rows a thread of a tile, scanned by every block
 
 struct TabParams {
@@ -116,12 +120,80 @@ __device__ __forceinline__ int tab_owner(const T* off, int lo, int hi, long long
 struct TabWindow {
   const int32_t *row, *page, *past;
   int first, n;
+  // where rows are taken request by request: the page that each one's cached tokens end in, and the free
+  // list's entries [free0, free0 + n_free)
+  const int32_t *open, *free_pages;
+  int free0, n_free;
 };
 
-// Rows base + lane, base + lane + 32, .. (count of them): a lane finds its first row's request by binary
-// search and walks on from there.
+// Where a request's rows go on for a while: the warp takes its request's rows [i0, i1) together.  Only the page
+// that the cached tokens end in is not a fresh one.
+__device__ __forceinline__ void tab_run(const TabParams& p, const TabWindow& w, int r, int i0, int i1) {
+  constexpr int BATCH = 2;
+  const int lane = threadIdx.x & 31, past = w.past[r], to_pos = past - w.row[r], log2 = p.P_log2, mask = (1 << log2) - 1;
+  int64_t* slots = p.slots + i0 + lane;
+  int32_t* positions = p.positions + i0 + lane;
+  int left = i1 - i0 - lane;             // rows of this lane and those behind it
+  if (past < 0) {
+    for (; left > 0; left -= 32, slots += 32, positions += 32) {
+      *slots = -1;
+      *positions = -1;
+    }
+    return;
+  }
+  const int before = (int)(((unsigned)past + mask) >> log2), pos0 = i0 + to_pos;
+  const unsigned n_pages = (unsigned)p.n_pages;
+  const int last = (i1 - 1 + to_pos) >> log2, to_free = w.page[r] - before;
+  // the free list's part that the tile's rows need is at hand, unless it is an uncommonly long one
+  const int first_free = to_free + max(before, pos0 >> log2) - w.free0, last_free = to_free + last - w.free0;
+  const int32_t* fresh = first_free >= 0 && last_free < w.n_free ? w.free_pages + (to_free - w.free0) : p.free_pages + to_free;
+  int32_t* entries = p.table + (long long)(w.first + r) * p.max_blocks;
+  const int open = w.open[r];
+  for (int b = max(before, (pos0 + mask) >> log2) + lane; b <= last; b += 32) {     // the fresh pages that begin here
+    const int page = fresh[b];
+    if ((unsigned)page < n_pages) entries[b] = page;
+  }
+  bool bad = false;
+  auto batch = [&](auto all, int pos) {
+    int page[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      page[k] = open;
+      const int blk = (pos + 32 * k) >> log2;
+      if ((decltype(all)::value || left > 32 * k) && blk >= before) page[k] = fresh[blk];
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const bool ok = (unsigned)page[k] < n_pages;
+      if (decltype(all)::value || left > 32 * k) {
+        slots[32 * k] = ok ? ((int64_t)page[k] << log2) + ((pos + 32 * k) & mask) : -1;
+        positions[32 * k] = ok ? pos + 32 * k : -1;
+        bad = bad || !ok;
+      }
+    }
+  };
+  int pos = pos0 + lane;
+  int whole = (i1 - i0) / (32 * BATCH);          // batches that every lane has all of
+  for (; whole > 0; --whole, left -= 32 * BATCH, pos += 32 * BATCH, slots += 32 * BATCH, positions += 32 * BATCH)
+    batch(std::true_type{}, pos);
+  batch(std::false_type{}, pos);
+  if (bad) set_status(p.status, ROCS_ERR_INDEX);
+}
+
+// Rows [base, base + 32 count) by one warp.  Request by request where each has 16 rows or more on average;
+// else row base + lane, base + lane + 32, ..: a lane finds its first row's request by binary search and
+// walks on from there.
+template <bool RUNS>
 __device__ __forceinline__ void tab_rows(const TabParams& p, const TabWindow& w, long long base, int count, long long n_rows) {
   const int mask = (1 << p.P_log2) - 1;
+  const long long stop = base + 32LL * count;
+  if (RUNS && stop <= n_rows && stop <= p.rows && stop <= w.row[w.n]) {
+    const int r0 = tab_owner(w.row, 0, w.n, base), r1 = tab_owner(w.row, r0, w.n, stop - 1);
+    if (r1 - r0 < 2 * count) {
+      for (int r = r0; r <= r1; ++r) tab_run(p, w, r, max(w.row[r], (int)base), min(w.row[r + 1], (int)stop));
+      return;
+    }
+  }
   int r = -1;                       // the row's request, counted from the window's first
   for (int k = 0; k < count; ++k) {
     const long long i = base + (threadIdx.x & 31) + 32 * k;
@@ -229,10 +301,10 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_inline_kernel(const Tab
   }
   __syncthreads();
   if (writer && threadIdx.x == 0) *p.pages_used = s_used;
-  const TabWindow w = {s_row, s_page, s_past, 0, p.B_R};
+  const TabWindow w = {s_row, s_page, s_past, 0, p.B_R, nullptr, nullptr, 0, 0};
   const long long tile = (long long)kTabThreads * kTabRows;
   for (long long t0 = blockIdx.x * tile; t0 < p.rows; t0 += gridDim.x * tile)
-    tab_rows(p, w, t0 + (threadIdx.x >> 5) * (32 * kTabRows), kTabRows, ta);
+    tab_rows<false>(p, w, t0 + (threadIdx.x >> 5) * (32 * kTabRows), kTabRows, ta);
 }
 
 // Few rows (at most four a request on average): one block, each request's rows written by its own thread,
@@ -369,8 +441,9 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_scan_kernel(const TabPa
   if (threadIdx.x == 0 && s_used > 0) atomicMax(p.pages_used, s_used);   // a maximum: any order
 }
 
-__global__ void __launch_bounds__(kTabThreads) kv_tables_expand_kernel(const TabParams p) {
-  __shared__ int32_t s_row[kTabThreads + 1], s_page[kTabThreads], s_past[kTabThreads];
+__global__ void __launch_bounds__(kTabThreads, 4) kv_tables_expand_kernel(const TabParams p) {
+  __shared__ int32_t s_row[kTabThreads + 1], s_page[kTabThreads], s_past[kTabThreads], s_open[kTabThreads], s_free[kTabFree];
+  __shared__ int s_free0;
   grid_dependency_wait();
   const long long n_rows = p.row_off[p.B_R], tile = (long long)p.tile_rows * kTabThreads;
   for (long long t0 = blockIdx.x * tile; t0 < p.rows; t0 += gridDim.x * tile) {
@@ -390,12 +463,21 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_expand_kernel(const Tab
       const TabReq q = tab_request(p, r);
       s_row[threadIdx.x] = p.row_off[r];
       s_page[threadIdx.x] = clip32(p.page_off[r]);
-      s_past[threadIdx.x] = q.bad || (q.need > 0 && p.page_off[r] + q.need > p.n_free) ? -1 : q.past;
+      const bool dead = q.bad || (q.need > 0 && p.page_off[r] + q.need > p.n_free);
+      s_past[threadIdx.x] = dead ? -1 : q.past;
       if ((int)threadIdx.x == n - 1) s_row[n] = p.row_off[r + 1];
+      const int mask = (1 << p.P_log2) - 1;
+      s_open[threadIdx.x] = !dead && q.rows > 0 && (q.past & mask) != 0 ? p.table[(long long)r * p.max_blocks + (q.past >> p.P_log2)] : -1;
+      // the free list's entry of the tile's first row, or of the first after it
+      if (threadIdx.x == 0)
+        s_free0 = s_page[0] + (dead ? 0 : max(0, (int)((q.past + (t0 - s_row[0])) >> p.P_log2) - q.before));
     }
     __syncthreads();
-    const TabWindow w = {s_row, s_page, s_past, lo, n};
-    tab_rows(p, w, t0 + (threadIdx.x >> 5) * (32 * p.tile_rows), p.tile_rows, n_rows);
+    const int free0 = s_free0, n_free = (int)min((long long)kTabFree, min((tile >> p.P_log2) + n + 1, (long long)p.n_free - free0));
+    for (int i = threadIdx.x; i < n_free; i += kTabThreads) s_free[i] = p.free_pages[free0 + i];
+    __syncthreads();
+    const TabWindow w = {s_row, s_page, s_past, lo, n, s_open, s_free, free0, n_free};
+    tab_rows<true>(p, w, t0 + (threadIdx.x >> 5) * (32 * p.tile_rows), p.tile_rows, n_rows);
   }
 }
 

@@ -111,6 +111,29 @@ def test_block_tables_many_empty_and_some_long_requests(R, B):
     check_tables(R, past, new, page, order[k:], len(order), table, int(new.sum()) + 3)
 
 
+@pytest.mark.parametrize("B,page,new_top,pad", [(2500, 16, 300, 9), (2100, 64, 900, 0), (2100, 16, 19000, 5)])
+def test_block_tables_long_rows_of_many_requests(R, B, page, new_top, pad):
+    """Rows taken request by request, among them unusable requests and bad pages; the last case has tiles whose
+    part of the free list is longer than the threads keep at hand."""
+    g = np.random.default_rng(B + new_top)
+    new = g.integers(0, new_top + 1, B)
+    past = g.integers(0, 200, B)
+    held, after = (past + page - 1) // page, (past + new + page - 1) // page
+    order = g.permutation(int(after.sum()) + 5).astype(np.int32)
+    table = np.full((B, int(after.max())), -1, np.int32)
+    k = 0
+    for r in range(B):
+        table[r, :held[r]] = order[k:k + held[r]]
+        k += held[r]
+    free = order[k:]
+    check_tables(R, past, new, page, free, len(order), table, int(new.sum()) + pad)
+    past[[7, 1000]] = -1, 10 ** 9                    # unusable
+    table[[20, 1500], held[[20, 1500]] - 1] = -7, len(order)
+    free[[3, len(free) // 2]] = -1, len(order)
+    free = free[:len(free) - 400]                    # the last requests get nothing
+    check_tables(R, past, new, page, free, len(order), table, int(new.sum()) - 1)
+
+
 @pytest.mark.parametrize("B", [40, 5000])
 def test_block_tables_bad_requests(R, B):
     """Negative and overlong lengths, a free list that runs out, bad pages in the list and in the table,
@@ -499,6 +522,21 @@ def test_attention_more_requests_than_are_listed(R, q, d, causal):
         keep[c.offsets[r]:c.offsets[r + 1]] = False
     close(got[keep], want[keep], mag[keep])
     assert (got[~keep] == 9).all()
+
+
+@pytest.mark.parametrize("d,q", [(32, 40), (64, 150), (128, 65)])
+def test_attention_runs_of_empty_and_tiny_histories(R, d, q):
+    """Hundreds of histories of no, one or a few blocks in a row: the tiles of one block of threads follow each other."""
+    B = 1500
+    g = np.random.default_rng(d)
+    lens = g.choice([0, 0, 0, 0, 1, 63, 64, 65, 130], B)
+    lens[200:900] = 0
+    lens[1200:] = g.integers(1, 3, 300)
+    c = Cached(19, g.integers(q - 8, q + 8, B), lens, 1, 1, d, 16)
+    for causal in (0, 1):
+        got = c.run(R, d ** -0.5, causal)
+        assert status(R) == 0
+        close(got, *c.want(d ** -0.5, causal))
 
 
 @pytest.mark.parametrize("counts,lens,d,share,page", [
