@@ -600,6 +600,27 @@ def test_attention_no_rows(R):
     assert status(R) == 0
 
 
+@pytest.mark.parametrize("d,page", [(32, 16), (64, 64), (128, 128)])
+def test_attention_many_rows_cache_offsets_past_32_bits(R, d, page):
+    """150 candidates against the last two pages of a cache of 5 GB."""
+    from request_candidate_sharing_b200 import rocs
+    H = 8
+    rec = KC.record_bytes(page, d)
+    n_pages = 5 * 2 ** 30 // (H * rec)
+    cache = torch.empty(n_pages, H, rec, dtype=torch.uint8, device="cuda")
+    length = 2 * page - 3
+    c = Cached(20, [150], [length], H, 1, d, page)
+    cache[-2:].copy_(torch.from_numpy(c.cache[c.table[0, :2]]))
+    desc = rocs.Kv4Desc(n_pages, page, H, d)
+    out = torch.zeros(150, H * d, dtype=torch.bfloat16, device="cuda")
+    q, table = bf16(c.Q).reshape(150, -1).cuda(), dev_i32([[n_pages - 2, n_pages - 1]])
+    n = R.rocs_dca_cross_attn_kv4_workspace(desc, H, 1, 150, 2)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    R.rocs_dca_cross_attn_kv4(desc, q, H * d, H, cache, table, 2, dev_i32([length]), dev_i32([0, 150]), 1, 150, 0.1, 1, out, H * d, ws, n, stream())
+    assert status(R) == 0
+    close(host(out).reshape(150, H, d), *c.want(0.1, 1))
+
+
 def test_attention_cache_offsets_past_32_bits(R):
     """The last page of a cache of 5 GB."""
     from request_candidate_sharing_b200 import rocs
