@@ -11,9 +11,9 @@
 // further on, no shuffles; else (neighbouring pairs, or past d_rot) eight neighbours.  A head is d / 8
 // lanes of one warp, the mean a few shuffles, a warp covers 32 / lanes heads of a row at a time; the
 // arithmetic is on packed fp32 pairs, and lanes past d_rot turn by nothing.
-// A warp takes up to four (row, unit of heads) items of the queries or of the keys, and asks for their
+// A warp takes a few (row, unit of heads) items of the queries or of the keys, and asks for their
 // elements, positions and then angles before it works on the first; nothing loops, so that the registers
-// allow many warps.  For 524288 rows of 8 + 8 heads of 32: 201 us (82% of the measured copy bandwidth);
+// allow many warps.  For 524288 rows of 8 + 8 heads of 32: 190 us (87% of the measured copy bandwidth);
 // 295 us where warps walked over many rows with the next elements in flight, 253 us where each item
 // chose its side.  fp32, 30011 rows of 16 + 2 heads of 128: 91 us (94%).
 #include "common.cuh"
@@ -41,13 +41,14 @@ struct QkParams {
   float eps, inv_d;
   unsigned blocks_q;       // blocks of the queries; the keys' follow
   int items;               // of a warp
+  bool full;               // the head fills its lanes and turns as a whole
   int* status;
 };
 
 // A lane's eight elements as they lie in memory: two runs of four.
 template <typename E> struct QkRaw;
 template <> struct QkRaw<__nv_bfloat16> {
-  static constexpr int ITEMS = 4;       // of a warp, where there are many
+  static constexpr int ITEMS = 3, ITEMS_PARTIAL = 4;      // of a warp, where there are many; without FULL
   uint2 a, b;
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int oa, int ob) {
     a = __ldcs(reinterpret_cast<const uint2*>(p + oa));
@@ -80,7 +81,7 @@ template <> struct QkRaw<__nv_bfloat16> {
   }
 };
 template <> struct QkRaw<float> {
-  static constexpr int ITEMS = 2;
+  static constexpr int ITEMS = 2, ITEMS_PARTIAL = 2;
   float4 a, b;
   __device__ __forceinline__ void load(const float* p, int oa, int ob) {
     a = __ldcs(reinterpret_cast<const float4*>(p + oa));
@@ -124,7 +125,7 @@ __device__ __forceinline__ uint64_t qk_fma(uint64_t a, uint64_t b, uint64_t c) {
 // T lanes a head (a power of two, T * 8 >= d).  HALVES: pairs are (t, t + d_rot / 2).  FULL: d = 8 T and
 // all of it turns, the usual case, without predicates.  N items a warp.
 template <typename E, int T, bool HALVES, bool FULL, int N>
-__global__ void __launch_bounds__(256, N == 4 ? 3 : N == 2 ? 4 : 6) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(256, N == 1 ? 6 : N == 4 ? 3 : 4) qk_norm_rope_kernel(const QkParams p) {
   constexpr int HEADS = 32 / T;
   const int lane = threadIdx.x & 31, sub = lane & (T - 1), hw = lane / T;
   const bool key = blockIdx.x >= p.blocks_q;
@@ -212,19 +213,18 @@ __global__ void __launch_bounds__(256, N == 4 ? 3 : N == 2 ? 4 : 6) qk_norm_rope
   }
 }
 
-template <typename E, int T, int N>
+template <typename E, int T, bool FULL, int N>
 void qk_launch_n(const QkParams& p, bool halves, unsigned grid, cudaStream_t s) {
-  const bool full = p.d == 8 * T && p.d_rot == p.d;
-  if (halves && full) qk_norm_rope_kernel<E, T, true, true, N><<<grid, 256, 0, s>>>(p);
-  else if (halves) qk_norm_rope_kernel<E, T, true, false, N><<<grid, 256, 0, s>>>(p);
-  else if (full) qk_norm_rope_kernel<E, T, false, true, N><<<grid, 256, 0, s>>>(p);
-  else qk_norm_rope_kernel<E, T, false, false, N><<<grid, 256, 0, s>>>(p);
+  if (halves) qk_norm_rope_kernel<E, T, true, FULL, N><<<grid, 256, 0, s>>>(p);
+  else qk_norm_rope_kernel<E, T, false, FULL, N><<<grid, 256, 0, s>>>(p);
 }
 
 template <typename E, int T>
 void qk_launch(const QkParams& p, bool halves, unsigned grid, cudaStream_t s) {
-  if (p.items == 1) qk_launch_n<E, T, 1>(p, halves, grid, s);
-  else qk_launch_n<E, T, QkRaw<E>::ITEMS>(p, halves, grid, s);
+  if (p.full && p.items == 1) qk_launch_n<E, T, true, 1>(p, halves, grid, s);
+  else if (p.full) qk_launch_n<E, T, true, QkRaw<E>::ITEMS>(p, halves, grid, s);
+  else if (p.items == 1) qk_launch_n<E, T, false, 1>(p, halves, grid, s);
+  else qk_launch_n<E, T, false, QkRaw<E>::ITEMS_PARTIAL>(p, halves, grid, s);
 }
 
 template <typename E>
@@ -257,9 +257,14 @@ rocs_status launch_qk_norm_rope(rocs_context* ctx, const rocs_qk_desc& d, const 
   const int heads = 32 / T;
   long long blocks[2];
   for (QkSide& sd : p.side) sd.units = (sd.H + heads - 1) / heads;
-  // one item a warp until the warps fill the GPU (1.7 instead of 2.2 us on 512 rows), then several
+  p.full = d.d_h == 8 * T && d.d_rot == d.d_h;
+  // One item a warp until the warps fill the GPU (1.7 instead of 2.2 us on 512 rows), then several: bf16 three
+  // and four blocks an SM where the head is full (190 us on 524288 rows of 16 heads of 32, four and three
+  // 201), else four and three (131072 rows of 20 heads of 128 of which 64 turn: 286 us, three and three 297).
   const long long all = d.rows * (p.side[0].units + p.side[1].units);
-  p.items = all < 48LL * ctx->num_sms ? 1 : d.io == ROCS_BF16 ? QkRaw<__nv_bfloat16>::ITEMS : QkRaw<float>::ITEMS;
+  p.items = all < 48LL * ctx->num_sms ? 1
+            : d.io != ROCS_BF16       ? (p.full ? QkRaw<float>::ITEMS : QkRaw<float>::ITEMS_PARTIAL)
+                                      : (p.full ? QkRaw<__nv_bfloat16>::ITEMS : QkRaw<__nv_bfloat16>::ITEMS_PARTIAL);
   const int items = 8 * p.items;      // of a block
   for (int i = 0; i < 2; ++i) {
     QkSide& sd = p.side[i];
