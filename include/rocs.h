@@ -356,7 +356,8 @@ rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc
  *            the other calls skip.
  *   pages_used [1] int32, written: how many entries of free_pages were taken.
  * A request whose lengths are negative or exceed max_blocks * P tokens, or whose pages exceed what
- * free_pages still holds, takes none: its rows (new_len of them, none if negative) get -1, its kv_len
+ * free_pages still holds, takes none (those behind it go on from the same entry, so a smaller one may
+ * fit): its rows (new_len of them, none if negative) get -1, its kv_len
  * stays past_len (0 if past_len itself is unusable) and the device status becomes ROCS_ERR_COUNTS;
  * new rows that sum to more than `rows` set it too (those beyond are not written, nor the table entries
  * of pages that begin in them).  A page outside [0, n_pages), in the table or the free list, gives its

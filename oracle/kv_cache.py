@@ -20,7 +20,7 @@ def block_tables(past, new, page, free, n_pages, table, rows):
     max_blocks = table.shape[1]
     kv_len, offsets = np.zeros(len(new), np.int32), np.zeros(len(new) + 1, np.int32)
     slots, positions = np.full(rows, -1, np.int64), np.full(rows, -1, np.int32)
-    row = taken = used = 0
+    row = taken = 0
     st = set()
     for r, n in enumerate(int(x) for x in new):
         p = int(past[r])
@@ -50,14 +50,12 @@ def block_tables(past, new, page, free, n_pages, table, rows):
                     slots[row + j], positions[row + j] = int(pg) * page + o, p + j
                 else:
                     st.add("index")
-            if need:
-                used = taken + need
-        taken += need
+            taken += need                        # one that does not fit leaves the pages to those behind it
         row += max(n, 0)
     offsets[len(new)] = row
     if row > rows:
         st.add("counts")
-    return table, kv_len, offsets, slots, positions, used, st
+    return table, kv_len, offsets, slots, positions, taken, st
 
 
 # ---- head norms and rotation ---------------------------------------------------------------------

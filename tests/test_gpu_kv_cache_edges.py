@@ -1,0 +1,68 @@
+"""The 4-bit history cache's calls where they go wrong most easily, against the float64 oracle: pages that run
+out between requests of all sizes."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv_cache import R, check_tables, run_tables, status  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- pages that run out -----------------------------------------------------------------------------------
+@pytest.mark.parametrize("rows", [91, 400])            # one thread a request; tiles of rows
+def test_a_request_that_does_not_fit_leaves_the_pages_to_others(R, rows):  # noqa: F811
+    got = run_tables(R, None, np.array([20, 70, 1]), 16, np.array([8, 3, 6], np.int32), 10, np.full((3, 5), -1, np.int32), rows)
+    assert status(R) == 7
+    assert got["kv"].tolist() == [20, 0, 1] and got["off"].tolist() == [0, 20, 90, 91] and got["used"].tolist() == [3]
+    assert got["table"][:, :2].tolist() == [[8, 3], [-1, -1], [6, -1]] and (got["table"][:, 2:] == -1).all()
+    want = np.full(rows, -1)
+    want[:20], want[90] = [*range(128, 144), *range(48, 52)], 96
+    assert np.array_equal(got["slots"], want)
+    want[:20], want[90] = range(20), 0
+    assert np.array_equal(got["pos"], want)
+
+
+@pytest.mark.parametrize("B,new_top", [(2, 300), (33, 3), (33, 300), (700, 5), (700, 90), (2048, 4), (2048, 60), (2049, 60), (5000, 2), (5000, 60), (20000, 9)])
+def test_block_tables_run_out_between_requests_of_all_sizes(R, B, new_top):  # noqa: F811
+    """Small requests behind large ones, with little to a lot of the free list there: each takes what the ones in
+    front of it left."""
+    g = np.random.default_rng(B + new_top)
+    page = 16
+    new = np.minimum(np.round(np.exp(g.normal(np.log(new_top / 4 + 1), 1.5, B))).astype(np.int64), 40 * new_top)
+    past = g.integers(0, 60, B)
+    held, after = (past + page - 1) // page, (past + new + page - 1) // page
+    order = g.permutation(int(after.sum()) + 5).astype(np.int32)
+    table = np.full((B, int(after.max())), -1, np.int32)
+    k = 0
+    for r in range(B):
+        table[r, :held[r]] = order[k:k + held[r]]
+        k += held[r]
+    need = after - held
+    total = int(need.sum())
+    new_bad = np.array(new)
+    new_bad[g.integers(0, B)] = -3
+    for n in sorted({0, 1, int(need.max()) // 2, int(need.max()), total // 10, total // 2, total - 1, total}):
+        check_tables(R, past, new if n % 2 else new_bad, page, order[k:k + n], len(order), table, int(new.sum()) + 2)
+
+
+def test_block_tables_one_request_is_refused_a_turn(R):  # noqa: F811
+    """The needs go 1, n, 1, n - 1, 1, n - 2, ..: each large one finds a page too few after the small one before it."""
+    B, page = 3000, 16
+    new = np.ones(B, np.int64)
+    new[1::2] = page * (np.arange(B // 2)[::-1] + 1)
+    table = np.full((B, B // 2), -1, np.int32)
+    for n in (B // 2, B // 2 + 7, 40):
+        check_tables(R, None, new, page, np.arange(n, dtype=np.int32), n, table, int(new.sum()))
+
+
+def test_block_tables_run_out_far_behind(R):  # noqa: F811
+    """More requests than one pass over the sums of their chunks covers: the free list ends far behind, near the
+    start, or a page before the last request."""
+    B, page = 300000, 16
+    g = np.random.default_rng(1)
+    new = g.integers(0, 4, B)
+    new[g.integers(0, B, 3000)] = 40
+    table = np.full((B, 3), -1, np.int32)
+    total = int(((new + 15) // 16).sum())
+    for n in (total - 1, total - 3000, total // 1000):
+        check_tables(R, None, new, page, g.permutation(n).astype(np.int32), n, table, int(new.sum()))

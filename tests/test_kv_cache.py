@@ -265,3 +265,14 @@ def test_attention_refusals(rocs, h, change):
     d = rocs.Kv4Desc(40, 64, change.get("H_kv", 8), 32)
     assert rocs._lib_attn4(h, ctypes.byref(d), *{**AT, **{k: v for k, v in change.items() if k != "H_kv"}}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
     assert "rocs_dca_cross_attn_kv4" in rocs.rocs_last_error()
+
+
+# ---- pages that run out -----------------------------------------------------------------------------
+def test_block_tables_requests_behind_one_that_does_not_fit():
+    # pages of 16, three free: 20 tokens take two, 70 would take five and get none, 1 takes the third, 5 find nothing
+    table = np.full((4, 5), -1, np.int32)
+    t, kv, off, slots, pos, used, st = KC.block_tables(None, [20, 70, 1, 5], 16, [8, 3, 6], 10, table, 96)
+    assert kv.tolist() == [20, 0, 1, 0] and off.tolist() == [0, 20, 90, 91, 96] and used == 3 and st == {"counts"}
+    assert t[:, :2].tolist() == [[8, 3], [-1, -1], [6, -1], [-1, -1]] and (t[:, 2:] == -1).all()
+    assert slots[:20].tolist() == [*range(128, 144), *range(48, 52)] and slots[90] == 96 and pos[90] == 0
+    assert (slots[20:90] == -1).all() and (slots[91:] == -1).all() and (pos[20:90] == -1).all() and (pos[91:] == -1).all()
