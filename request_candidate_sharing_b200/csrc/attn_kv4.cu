@@ -177,11 +177,13 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
   }
 
   float o[MT][NT][4];
-  float m_run[NT][2], l_run[NT][2];
+  // sums of the weights as they enter the product, rounded (numerator and denominator weigh alike): a further
+  // row tile of that product, of ones, whose rows are all the sum
+  float m_run[NT][2], l_run[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
-    l_run[nt][0] = l_run[nt][1] = 0.f;
+    l_run[nt][0] = l_run[nt][1] = l_run[nt][2] = l_run[nt][3] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -309,8 +311,9 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
             const float m_new = fmaxf(m_run[nt][e], mx[nt][e]);
             corr[e] = m_new == -INFINITY ? 1.f : ex2_approx(m_run[nt][e] - m_new);
             m_run[nt][e] = m_new;
-            l_run[nt][e] *= corr[e];
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l_run[nt][e] *= corr[e & 1];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -329,10 +332,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
           float e4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4[e] = ex2_approx(fmaf(s[t][nt][e], p.sl2, neg[e & 1]));
-          l_run[nt][0] += e4[0] + e4[2];
-          l_run[nt][1] += e4[1] + e4[3];
           pf[t][nt][0] = transpose8x8(pack_bf16x2(e4[0], e4[1]));
           pf[t][nt][1] = transpose8x8(pack_bf16x2(e4[2], e4[3]));
+          constexpr uint32_t ONES[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+          mma_bf16_16816(l_run[nt], ONES, pf[t][nt][0], pf[t][nt][1]);
         }
       }
       // O^T += V^T P^T
@@ -400,15 +403,11 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = l_run[nt][e];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    for (int e = 0; e < 2; ++e)
       if (g == 0) {
         s_m[warp][nt * 8 + 2 * tq + e] = m_run[nt][e];
-        s_l[warp][nt * 8 + 2 * tq + e] = l;
+        s_l[warp][nt * 8 + 2 * tq + e] = l_run[nt][e];
       }
-    }
   __syncthreads();
   float* so = reinterpret_cast<float*>(ka_smem);        // [warp][row][D]
 #pragma unroll

@@ -92,18 +92,6 @@ __device__ __forceinline__ uint4 kt_order(uint4 x) {
                     __byte_perm(x.y, x.w, 0x7632));
 }
 
-// (a, b) added to a pair of running sums, and the pair's sum.
-__device__ __forceinline__ void add2(uint64_t& s, float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s) : "l"(v));
-}
-__device__ __forceinline__ float sum2(uint64_t s) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(s));
-  return a + b;
-}
-
 template <int D>
 __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc_kernel(const KaParams p) {
   using C = KtCfg<D>;
@@ -239,7 +227,9 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
         m_cur = m_new;
         // a row that has seen nothing yet weighs nothing; one with an infinite score is undefined
         const float neg = m_new == -INFINITY ? 0.f : m_new == INFINITY ? NAN : -m_new;
-        uint64_t rs = 0;   // two running sums
+        // the sum is of the weights as they enter the product, rounded: then numerator and denominator
+        // weigh alike
+        float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
@@ -249,12 +239,14 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
             ffma2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]), sl2, neg, x0, x1);
             p0 = ex2_approx(x0);
             p1 = ex2_approx(x1);
-            add2(rs, p0, p1);
-            pk[e >> 1] = pack_bf16x2(p0, p1);
+            const uint32_t w = pack_bf16x2(p0, p1);
+            rs0 = add_lo(w, rs0);
+            rs1 = add_hi(w, rs1);
+            pk[e >> 1] = w;
           }
           tmem_st_32x32b_x16(saddr + c * 16, pk);
         }
-        l += sum2(rs);
+        l += rs0 + rs1;
         tmem_st_wait();
       }
       // no softmax warp is more than a block ahead of another, and the producers reach block j + 4, the

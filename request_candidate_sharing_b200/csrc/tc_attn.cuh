@@ -85,4 +85,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// c + the low / high element of a bf16 pair, in fp32.
+__device__ __forceinline__ float add_lo(uint32_t pair, float c) {
+  float d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %2;\n\t}" : "=f"(d) : "r"(pair), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float add_hi(uint32_t pair, float c) {
+  float d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, h, %2;\n\t}" : "=f"(d) : "r"(pair), "f"(c));
+  return d;
+}
+
 }  // namespace rocs

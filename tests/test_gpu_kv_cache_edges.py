@@ -1,9 +1,12 @@
 """The 4-bit history cache's calls where they go wrong most easily, against the float64 oracle: pages that run
-out between requests of all sizes."""
+out between requests of all sizes, and weights that round alike."""
+import math
+
 import numpy as np
 import pytest
 
-from tests.test_gpu_kv_cache import R, check_tables, run_tables, status  # noqa: F401
+from oracle import kv_cache as KC
+from tests.test_gpu_kv_cache import Cached, R, check_tables, run_tables, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +69,34 @@ def test_block_tables_run_out_far_behind(R):  # noqa: F811
     total = int(((new + 15) // 16).sum())
     for n in (total - 1, total - 3000, total // 1000):
         check_tables(R, None, new, page, g.permutation(n).astype(np.int32), n, table, int(new.sum()))
+
+
+# ---- attention ----------------------------------------------------------------------------------------------------
+def fill(c, K, V):
+    """Puts K and V [H, tokens, d] of every request's history (the same for all) into the cache of a Cached."""
+    for r, n in enumerate(c.lens):
+        t = np.arange(n)
+        slots = c.table[r, t // c.page].astype(np.int64) * c.page + t % c.page
+        c.cache = KC.append(c.cache, c.page, K[:, :n].transpose(1, 0, 2), V[:, :n].transpose(1, 0, 2), slots)
+    c.K, c.V = KC.values(c.cache, c.page, c.d)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("counts,lens,share", [([1, 1], [64, 200], 1), ([3, 2], [500, 64], 4), ([20, 9], [128, 65], 1), ([1], [9000], 2),
+                                               ([130, 40], [300, 64], 1), ([50], [5000], 2)])
+def test_attention_of_equal_values_gives_that_value(R, counts, lens, d, share):  # noqa: F811
+    """Every value is 63/32, so every output is, whatever the weights are, as long as their sum is of the weights
+    that multiply the values.  One key in 64 has weight 1, the others 1/2 + 1.05 * 2^-9, which bf16 rounds up to
+    1/2 + 2^-8: divided by the sum of the unrounded weights the result would be 63/32 * (1 + 2^-8 * 0.93 or more),
+    past the middle (63/32 * (1 + 2^-9 * 1.016)) between 63/32 and the next bf16 number.  Sums and products carry
+    fp32 errors, far below that."""
+    c = Cached(31, counts, lens, 2, share, d, 64)
+    n = max(lens)
+    K, V = np.zeros((2, n, d)), np.full((2, n, d), 63 / 32)
+    K[:, :, 0], K[:, :, 1] = 6, 7                        # element 1 fixes the group's scale at 1
+    K[:, ::64, 0] = 7
+    fill(c, K, V)
+    c.Q = np.zeros_like(c.Q)
+    c.Q[:, :, 0] = 1
+    got = c.run(R, -math.log(0.5 + 1.05 * 2.0 ** -9), 0)
+    assert status(R) == 0 and (got == 63 / 32).all(), np.unique(got)
