@@ -432,7 +432,7 @@ rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, con
  * workspace: rocs_dca_cross_attn_kv4_workspace bytes (may be 0), 256-byte aligned, for this call alone until
  * its work is done: calls that may overlap (other streams, graphs replayed side by side) need one each.
  * O may not overlap Q or the other inputs.  Limits: strides multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256;
- * rows * H_q <= 2^31 - 256; 1 <= B_R <= 2^24 with B_R * H_kv < 2^30; scale finite. */
+ * rows * H_q <= 2^31 - 256; 1 <= B_R <= 2^24 with B_R * H_kv < 2^30; |scale| <= 2^126. */
 rocs_status rocs_dca_cross_attn_kv4_workspace(rocs_handle_t handle, const rocs_kv4_desc* desc, int32_t H_q,
                                               int32_t B_R, int64_t rows, int32_t max_blocks, size_t* bytes);
 rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t handle, const rocs_kv4_desc* desc, const void* Q, int64_t ld_Q,

@@ -1045,7 +1045,8 @@ extern "C" rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t h, const rocs_kv4_d
   ROCS_REQUIRE(ld_Q >= width && ld_O >= width && ld_Q % 8 == 0 && ld_O % 8 == 0,
                "%s: row strides must be multiples of 8, at least H_q * d_h", who);
   ROCS_REQUIRE(aligned16(Q) && aligned16(O) && aligned16(cache), "%s: misaligned", who);
-  ROCS_REQUIRE(std::isfinite(scale), "%s: scale not finite", who);
+  // (its product with log2(e) stays finite)
+  ROCS_REQUIRE(std::fabs(scale) <= 0x1p126f, "%s: scale not finite, or beyond 2^126", who);
   ROCS_REQUIRE(causal == 0 || causal == 1, "%s: causal must be 0 or 1", who);
   ROCS_REQUIRE((((uintptr_t)block_table | (uintptr_t)kv_len | (uintptr_t)offsets) & 3) == 0, "%s: misaligned", who);
   ROCS_TRY(check_current_device(h, who));

@@ -43,7 +43,6 @@ namespace {
 
 constexpr int KA_WARPS = 4;
 constexpr int kTcRows = 32;     // packed rows a request above which the 128-row tensor-core tiles pay
-constexpr float kKaLazyLog2 = 8.0f;   // a row's reference maximum moves when a chunk exceeds it by this much
 
 template <int D>
 struct KaCfg {
@@ -297,8 +296,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
           float m = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
 #pragma unroll
           for (int t = 1; t < ST; ++t) m = fmax3(m, s[t][nt][e], s[t][nt][e + 2]);
-          mx[nt][e] = m * p.sl2;
-          moves = moves || mx[nt][e] > m_run[nt][e] + kKaLazyLog2;
+          mx[nt][e] = m;
+          moves = moves || m > m_run[nt][e] + p.lazy;
         }
       if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], x));
             const float m_new = fmaxf(m_run[nt][e], mx[nt][e]);
-            corr[e] = m_new == -INFINITY ? 1.f : ex2_approx(m_run[nt][e] - m_new);
+            corr[e] = m_new == -INFINITY ? 1.f : ex2_approx((m_run[nt][e] - m_new) * p.sl2);
             m_run[nt][e] = m_new;
           }
 #pragma unroll
@@ -320,18 +319,35 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
             for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
         }
       }
+      float neg[NT][2];
+      bool far = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          neg[nt][e] = m_run[nt][e] == -INFINITY ? 0.f : -m_run[nt][e] * p.sl2;   // nothing seen yet: weights of 0
+          far = far || !(fabsf(neg[nt][e]) < kKaFarLog2);
+        }
+      if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+#pragma unroll
+            for (int t = 0; t < ST; ++t) s[t][nt][e] -= ref;
+            neg[nt][e & 1] = 0.f;
+          }
+      }
       // weights and their sums; P^T in the operand's layout
       uint32_t pf[ST][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float neg[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) neg[e] = m_run[nt][e] == -INFINITY ? 0.f : -m_run[nt][e];   // nothing seen yet: weights of 0
 #pragma unroll
         for (int t = 0; t < ST; ++t) {
           float e4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) e4[e] = ex2_approx(fmaf(s[t][nt][e], p.sl2, neg[e & 1]));
+          for (int e = 0; e < 4; ++e) e4[e] = ex2_approx(fmaf(s[t][nt][e], p.sl2, neg[nt][e & 1]));
           pf[t][nt][0] = transpose8x8(pack_bf16x2(e4[0], e4[1]));
           pf[t][nt][1] = transpose8x8(pack_bf16x2(e4[2], e4[3]));
           constexpr uint32_t ONES[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
     const float ref = top == -INFINITY ? 0.f : top;
     float l = 0.f, x = 0.f, y = 0.f;
     for (int w = 0; w < p.per_item; ++w) {
-      const float f = ex2_approx(s_m[w0 + w][row] - ref);
+      const float f = ex2_approx((s_m[w0 + w][row] - ref) * p.sl2);
       const float2 v = *reinterpret_cast<const float2*>(so + ((w0 + w) * T + row) * D + d);
       l = fmaf(f, s_l[w0 + w][row], l);
       x = fmaf(f, v.x, x);
@@ -486,11 +502,11 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, in
         float m = top;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[i].x);
-        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx(top - ref);
+        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx((top - ref) * p.sl2);
         l *= f; x *= f; y *= f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = ex2_approx(ml[i].x - ref);
+          const float e = ex2_approx((ml[i].x - ref) * p.sl2);
           l = fmaf(e, ml[i].y, l);
           x = fmaf(e, v[i].x, x);
           y = fmaf(e, v[i].y, y);
@@ -510,11 +526,11 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const KaParams p, in
         float m = top;
 #pragma unroll
         for (int g = 1; g < GROUPS; ++g) m = fmaxf(m, s_part[g][D]);
-        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx(top - ref);
+        const float ref = m == -INFINITY ? 0.f : m, f = ex2_approx((top - ref) * p.sl2);
         l *= f; x *= f; y *= f;
 #pragma unroll
         for (int g = 1; g < GROUPS; ++g) {
-          const float e = ex2_approx(s_part[g][D] - ref);
+          const float e = ex2_approx((s_part[g][D] - ref) * p.sl2);
           l = fmaf(e, s_part[g][D + 1], l);
           x = fmaf(e, s_part[g][d], x);
           y = fmaf(e, s_part[g][d + 1], y);
@@ -832,7 +848,8 @@ rocs_status launch_attn_kv4(rocs_context* ctx, const rocs_kv4_desc& d, const voi
   p.P_log2 = 31 - __builtin_clz((unsigned)d.page_size);
   p.n_pages = d.n_pages;
   // a negative scale turns the queries round, so that the largest product is the largest score
-  p.sl2 = fmaxf(fabsf(scale) * 1.4426950408889634f, FLT_MIN);
+  p.sl2 = fmaxf(fabsf(scale) * 1.4426950408889634f, FLT_TRUE_MIN);
+  p.lazy = fminf(kKaLazyLog2 / p.sl2, FLT_MAX);
   p.q_flip = scale < 0.f ? 0x80008000u : 0u;
   p.causal = causal;
   p.O = (__nv_bfloat16*)O;

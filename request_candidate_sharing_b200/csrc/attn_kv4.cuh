@@ -9,6 +9,11 @@
 
 namespace rocs {
 
+// A row's reference (raw score, unscaled) moves when a weight would exceed 2^kKaLazyLog2.  A weight is 2 to
+// s * sl2 - ref * sl2 in one fused step while the second product is below kKaFarLog2, where its rounding is below
+// 2^-14; beyond, the difference is taken first, or the largest weight itself would round to nothing or infinity.
+constexpr float kKaLazyLog2 = 8.0f, kKaFarLog2 = 1024.0f;
+
 // A block's work: tile `first` .. (packed rows) of request r, whose n_r query rows begin at q0 and whose
 // keys are len; key units [c_lo, c_hi) of `unit` keys; the partial result's place, or -1 where the block
 // has all of the tile's keys and writes its output.
@@ -32,7 +37,8 @@ struct KaParams {
   int B_R;
   long long rows;
   int Hkv, share, P_log2, n_pages;
-  float sl2;            // |scale| * log2(e), at least the smallest normal number
+  float sl2;            // |scale| * log2(e), above zero (a masked score times it is an infinity)
+  float lazy;           // how far a score may exceed its row's reference: kKaLazyLog2 / sl2
   uint32_t q_flip;      // sign bits to flip in a query pair (a negative scale)
   int causal;
   __nv_bfloat16* O;
@@ -44,7 +50,7 @@ struct KaParams {
   int* counts;          // items, joins
   KaItem* items;
   KaJoin* joins;
-  float* part;          // [part][head][row][D] sums, and [part][head][row] (max, sum) pairs
+  float* part;          // [part][head][row][D] sums, and [part][head][row] (reference, sum) pairs
   float2* part_ml;
   int* status;
 };

@@ -42,7 +42,6 @@ namespace {
 
 constexpr int KT_ROWS = 128;
 constexpr int KT_KEYS = 64;
-constexpr float kKtLazyLog2 = 8.0f;
 // pauses between polls of the roles off the critical path, whose polls take issue slots from the softmax
 constexpr unsigned kKtProducerSleepNs = 200, kKtIssuerSleepNs = 32;
 
@@ -172,9 +171,9 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
     const uint32_t oaddr = o_tmem + lanes;
     const bool warp_live = a.first + warp * 32 < a.n;      // rows past the request's end are not computed
     const int limit = live ? ka_limit(p, a, m) : 0;
-    const float sl2 = p.sl2;
+    const float sl2 = p.sl2, lazy = p.lazy;
     float m_cur = -INFINITY, l = 0.f;
-    bool ok = true;
+    bool ok = true, far = false;
     for (int j = 0; j < n; ++j) {
       const int b = j & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], (j >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
@@ -202,31 +201,37 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
 #pragma unroll
           for (int t = 0; t < 8; ++t)
             mt[t] = fmax3(mt[t], __uint_as_float(v[(e + t) >> 5][(e + t) & 31]), __uint_as_float(v[(e + 8 + t) >> 5][(e + 8 + t) & 31]));
-        const float mx = fmax3(fmax3(mt[0], mt[1], mt[2]), fmax3(mt[3], mt[4], mt[5]), fmaxf(mt[6], mt[7])) * sl2;
-        // the reference maximum: the first block's, then moved (for the whole warp, whose O it
-        // rescales in tensor memory) when a row would produce weights above 2^8
-        float m_new = m_cur;
-        if (j == 0) {
-          m_new = mx;
-        } else if (__any_sync(0xffffffffu, mx > m_cur + kKtLazyLog2)) {
-          m_new = fmaxf(m_cur, mx);
-          const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m_cur - m_new);
-          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[b ^ 1], ((j - 1) >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
-          tc_fence_after();
+        const float mx = fmax3(fmax3(mt[0], mt[1], mt[2]), fmax3(mt[3], mt[4], mt[5]), fmaxf(mt[6], mt[7]));
+        // the reference: the first block's maximum, then moved (for the whole warp, whose O it rescales in
+        // tensor memory) when a row would produce weights above 2^8
+        if (j == 0 || __any_sync(0xffffffffu, mx > m_cur + lazy)) {
+          const float m_new = j == 0 ? mx : fmaxf(m_cur, mx);
+          if (j > 0) {
+            const float corr = m_new == -INFINITY ? 1.f : ex2_approx((m_cur - m_new) * sl2);
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[b ^ 1], ((j - 1) >> 1) & 1, p.status, &abort_flag))) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t w[16];
-            tmem_ld_32x32b_x16(oaddr + c * 16, w);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[16];
+              tmem_ld_32x32b_x16(oaddr + c * 16, w);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * corr);
-            tmem_st_32x32b_x16(oaddr + c * 16, w);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * corr);
+              tmem_st_32x32b_x16(oaddr + c * 16, w);
+            }
+            l *= corr;
           }
-          l *= corr;
+          m_cur = m_new;
+          far = __any_sync(0xffffffffu, m_new != -INFINITY && !(fabsf(m_new * sl2) < kKaFarLog2));
         }
-        m_cur = m_new;
-        // a row that has seen nothing yet weighs nothing; one with an infinite score is undefined
-        const float neg = m_new == -INFINITY ? 0.f : m_new == INFINITY ? NAN : -m_new;
+        // a row that has seen nothing yet weighs nothing; one with an infinite score is undefined (NaN)
+        const float ref = m_cur == -INFINITY ? 0.f : m_cur;
+        float neg = -ref * sl2;
+        if (far) {
+          neg = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e >> 5][e & 31] = __float_as_uint(__uint_as_float(v[e >> 5][e & 31]) - ref);
+        }
         // the sum is of the weights as they enter the product, rounded: then numerator and denominator
         // weigh alike
         float rs0 = 0.f, rs1 = 0.f;

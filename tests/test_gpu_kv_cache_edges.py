@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import kv_cache as KC
-from tests.test_gpu_kv_cache import Cached, R, check_tables, run_tables, status  # noqa: F401
+from tests.test_gpu_kv_cache import Cached, R, check_tables, close, run_tables, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,46 @@ def test_attention_of_equal_values_gives_that_value(R, counts, lens, d, share): 
     c.Q[:, :, 0] = 1
     got = c.run(R, -math.log(0.5 + 1.05 * 2.0 ** -9), 0)
     assert status(R) == 0 and (got == 63 / 32).all(), np.unique(got)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("counts,lens,share", [([1, 1], [64, 200], 1), ([3, 2], [500, 70], 4), ([20, 9], [128, 65], 1), ([1], [9000], 2),
+                                               ([130, 40], [300, 64], 1), ([50], [5000], 2)])
+@pytest.mark.parametrize("unit,scale", [(2.0 ** 34, 1.0), (2.0 ** 34, -0.7), (2.0 ** 115, 3.0), (2.0 ** 20, 2.0 ** 100), (1.0, 2.0 ** 126), (1.0, -8e37),
+                                        (2.0 ** 11, 0.3), (2.0 ** 118, 0.0), (2.0 ** 118, 1e-40), (2.0 ** 118, 2.5e-37)])
+def test_attention_of_scores_of_all_sizes(R, counts, lens, d, share, unit, scale):  # noqa: F811
+    """Scores from far above what fp32 tells apart by less than 2^7 to far below one.  A row's queries are 1, 2, .. in element 0,
+    keys are whole multiples of `unit` there, so scores are exact in fp32 and the tolerance is the usual one; the last
+    three scales make weights between 0.05 and 1 of scores near the largest number."""
+    c = Cached(32, counts, lens, 2, share, d, 64)
+    g = np.random.default_rng(5)
+    n = max(lens)
+    K, V = np.zeros((2, n, d)), g.integers(-7, 8, (2, n, d)).astype(np.float64)
+    V[:, :, ::32] = 7
+    K[:, :, 0], K[:, :, 1] = g.integers(-7, 8, (2, n)) * unit, 7 * unit
+    fill(c, K, V)
+    c.Q = np.zeros_like(c.Q)
+    c.Q[:, :, 0] = 1 + np.arange(c.rows)[:, None] % 4
+    got = c.run(R, scale, 0)
+    assert status(R) == 0
+    close(got, *c.want(np.float64(np.float32(scale)), 0))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("counts,lens,share", [([12, 13], [64, 200], 1), ([3, 2], [500, 70], 4), ([1], [9000], 2), ([130, 40], [300, 64], 1)])
+def test_attention_of_scores_far_from_zero(R, counts, lens, d, share):  # noqa: F811
+    """Every row's scores have a mean of its own, from 3 to 7000, and differ by halves: exact in fp32 (at most 17 bits), and so
+    is a difference of two."""
+    c = Cached(33, counts, lens, 2, share, d, 64)
+    g = np.random.default_rng(6)
+    n = max(lens)
+    K, V = np.zeros((2, n, d)), g.integers(-7, 8, (2, n, d)).astype(np.float64)
+    V[:, :, ::32] = 7
+    K[:, :, 0], K[:, :, 1] = 7, g.integers(-7, 8, (2, n))
+    fill(c, K, V)
+    c.Q = np.zeros_like(c.Q)
+    c.Q[:, :, 0] = 2.0 ** ((np.arange(c.rows)[:, None] + np.arange(2 * share)) % 12)
+    c.Q[:, :, 1] = 0.5
+    got = c.run(R, 0.5, 0)
+    assert status(R) == 0
+    close(got, *c.want(0.5, 0))

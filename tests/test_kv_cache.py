@@ -276,3 +276,10 @@ def test_block_tables_requests_behind_one_that_does_not_fit():
     assert t[:, :2].tolist() == [[8, 3], [-1, -1], [6, -1], [-1, -1]] and (t[:, 2:] == -1).all()
     assert slots[:20].tolist() == [*range(128, 144), *range(48, 52)] and slots[90] == 96 and pos[90] == 0
     assert (slots[20:90] == -1).all() and (slots[91:] == -1).all() and (pos[20:90] == -1).all() and (pos[91:] == -1).all()
+
+
+@pytest.mark.parametrize("scale", [1.01 * 2.0 ** 126, -1.01 * 2.0 ** 126])
+def test_attention_refuses_scales_whose_products_overflow(rocs, h, scale):
+    d = rocs.Kv4Desc(40, 64, 8, 32)
+    assert rocs._lib_attn4(h, ctypes.byref(d), *{**AT, "scale": scale}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
+    assert "2^126" in rocs.rocs_last_error()
