@@ -362,7 +362,7 @@ rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc
  * new rows that sum to more than `rows` set it too (those beyond are not written, nor the table entries
  * of pages that begin in them).  A page outside [0, n_pages), in the table or the free list, gives its
  * rows -1 and sets ROCS_ERR_INDEX.
- * The outputs may not overlap the inputs or one another.
+ * The outputs may not overlap the inputs or one another, nor the workspace any of them.
  * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 2048
  * requests), 16-byte aligned, for this call alone until its work is done.  Limits: 1 <= B_R <= 2^24;
  * 0 <= rows < 2^31 - 1; 0 <= n_free < 2^31 - 1; max_blocks >= 1 with max_blocks * P <= 2^31 - 256;
@@ -383,7 +383,8 @@ rocs_status rocs_kv_block_tables(rocs_handle_t handle, const int32_t* past_len, 
  *   Q [rows, H_q * d_h], K [rows, H_k * d_h] in `io` (bf16 or fp32), row strides ld_Q, ld_K elements:
  *     they may be slices of one wider buffer.  H_q or H_k may be 0 (that side is ignored, its pointers
  *     may be NULL).  Q_out, K_out in `io`, strides ld_Qo, ld_Ko; a side may be written in place (same
- *     pointer and stride), else its output may not overlap the inputs.
+ *     pointer and stride), else its output may not overlap the inputs.  No output may overlap the
+ *     gammas, cos_sin or the positions.
  *   gamma_q, gamma_k [d_h] fp32, or NULL for ones.  cos_sin [max_pos, d_rot] fp32 (cosines, then
  *     sines), so that far positions' angles are as exact as the caller makes them.
  *   positions [rows] int32, device: a row at -1 is padding, left as it was; any other position outside
@@ -431,7 +432,7 @@ rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, con
  * its keys are left out.  Rows behind the last request's are left as they were.
  * workspace: rocs_dca_cross_attn_kv4_workspace bytes (may be 0), 256-byte aligned, for this call alone until
  * its work is done: calls that may overlap (other streams, graphs replayed side by side) need one each.
- * O may not overlap Q or the other inputs.  Limits: strides multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256;
+ * O may not overlap Q or the other inputs, nor the workspace any of them.  Limits: strides multiples of 8, pointers 16-byte aligned; max_blocks * page_size <= 2^31 - 256;
  * rows * H_q <= 2^31 - 256; 1 <= B_R <= 2^24 with B_R * H_kv < 2^30; |scale| <= 2^126. */
 rocs_status rocs_dca_cross_attn_kv4_workspace(rocs_handle_t handle, const rocs_kv4_desc* desc, int32_t H_q,
                                               int32_t B_R, int64_t rows, int32_t max_blocks, size_t* bytes);

@@ -948,6 +948,8 @@ extern "C" rocs_status rocs_kv_block_tables(rocs_handle_t h, const int32_t* past
     set_error("%s: workspace of %zu bytes (16-byte aligned) needed", who, need);
     return ROCS_ERR_WORKSPACE;
   }
+  for (int i = 0; i < 6; ++i) ROCS_REQUIRE(!overlap(workspace, need, out[i], n_out[i]), "%s: the workspace overlaps an output", who);
+  for (int j = 0; j < 3; ++j) ROCS_REQUIRE(!overlap(workspace, need, in[j], n_in[j]), "%s: the workspace overlaps an input", who);
   ROCS_TRY(check_current_device(h, who));
   return launch_kv_tables(h, past_len, new_len, B_R, 31 - __builtin_clz((unsigned)page_size), free_pages, n_free,
                           n_pages, block_table, max_blocks, kv_len, row_offsets, slots, positions, rows, pages_used,
@@ -992,6 +994,12 @@ extern "C" rocs_status rocs_qk_norm_rope(rocs_handle_t h, const rocs_qk_desc* d,
       ROCS_REQUIRE(!rows_overlap(s.y, s.ldo * esz, width * esz, o.x, o.ld * esz, (int64_t)o.H * d->d_h * esz, d->rows),
                    "%s: an output overlaps an input", who);
     }
+    const size_t n_y = d->rows == 0 ? 0 : (size_t)((d->rows - 1) * s.ldo + width) * esz, n_g = (size_t)d->d_h * 4;
+    ROCS_REQUIRE(!overlap(s.y, n_y, d->H_q > 0 ? gamma_q : nullptr, n_g) &&
+                     !overlap(s.y, n_y, d->H_k > 0 ? gamma_k : nullptr, n_g) &&
+                     !overlap(s.y, n_y, cos_sin, (size_t)d->max_pos * d->d_rot * 4) &&
+                     !overlap(s.y, n_y, positions, (size_t)d->rows * 4),
+                 "%s: an output overlaps the gammas, the angles or the positions", who);
   }
   ROCS_REQUIRE(d->H_q == 0 || d->H_k == 0 ||
                    !rows_overlap(Q_out, ld_Qo * esz, (int64_t)d->H_q * d->d_h * esz, K_out, ld_Ko * esz,
@@ -1055,12 +1063,17 @@ extern "C" rocs_status rocs_dca_cross_attn_kv4(rocs_handle_t h, const rocs_kv4_d
     set_error("%s: workspace of %zu bytes (256-byte aligned) needed", who, need);
     return ROCS_ERR_WORKSPACE;
   }
-  const size_t n_o = rows == 0 ? 0 : (size_t)((rows - 1) * ld_O + width) * 2;
-  ROCS_REQUIRE(!rows_overlap(O, ld_O * 2, width * 2, Q, ld_Q * 2, width * 2, rows) &&
-                   !overlap(O, n_o, cache, (size_t)d->n_pages * d->H_kv * ((size_t)d->page_size * d->d_h * 9 / 8)) &&
-                   !overlap(O, n_o, block_table, (size_t)B_R * max_blocks * 4) &&
-                   !overlap(O, n_o, kv_len, (size_t)B_R * 4) && !overlap(O, n_o, offsets, (size_t)(B_R + 1) * 4),
-               "%s: the output overlaps an input", who);
+  const size_t n_o = rows == 0 ? 0 : (size_t)((rows - 1) * ld_O + width) * 2, n_q = rows == 0 ? 0 : (size_t)((rows - 1) * ld_Q + width) * 2;
+  const void* in[] = {cache, block_table, kv_len, offsets};
+  const size_t n_in[] = {(size_t)d->n_pages * d->H_kv * ((size_t)d->page_size * d->d_h * 9 / 8), (size_t)B_R * max_blocks * 4,
+                         (size_t)B_R * 4, (size_t)(B_R + 1) * 4};
+  ROCS_REQUIRE(!rows_overlap(O, ld_O * 2, width * 2, Q, ld_Q * 2, width * 2, rows), "%s: the output overlaps an input", who);
+  ROCS_REQUIRE(!overlap(workspace, need, O, n_o) && !overlap(workspace, need, Q, n_q),
+               "%s: the workspace overlaps the queries or the output", who);
+  for (int i = 0; i < 4; ++i) {
+    ROCS_REQUIRE(!overlap(O, n_o, in[i], n_in[i]), "%s: the output overlaps an input", who);
+    ROCS_REQUIRE(!overlap(workspace, need, in[i], n_in[i]), "%s: the workspace overlaps an input", who);
+  }
   return launch_attn_kv4(h, *d, Q, ld_Q, H_q, cache, block_table, max_blocks, kv_len, offsets, B_R, rows, scale,
                          causal, O, ld_O, workspace, (cudaStream_t)stream);
 }

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import kv_cache as KC
+from tests.gpu_util import stream
 from tests.test_gpu_kv_cache import Cached, R, check_tables, close, run_tables, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +144,19 @@ def test_attention_of_scores_far_from_zero(R, counts, lens, d, share):  # noqa: 
     got = c.run(R, 0.5, 0)
     assert status(R) == 0
     close(got, *c.want(0.5, 0))
+
+
+@pytest.mark.parametrize("at,inside", [("q", 0), ("q", 3840), ("o", 0), ("o", 3840), ("cache", 8960), ("table", 3840), ("kv", 0), ("off", 0)])
+def test_attention_refuses_a_workspace_over_its_tensors(R, at, inside):  # noqa: F811
+    """The addresses are far apart and of no memory: the call is refused before anything reads them."""
+    from request_candidate_sharing_b200 import rocs
+    d = rocs.Kv4Desc(16, 16, 1, 32)            # 9216 bytes
+    a = {k: (i + 1) << 32 for i, k in enumerate(("q", "o", "cache", "table", "kv", "off"))}
+    n = R.rocs_dca_cross_attn_kv4_workspace(d, 8, 1, 8, 1024)
+    assert 256 < n < 1 << 32
+    for ws in (a[at] + inside, a[at] + inside - n // 256 * 256):          # over the tensor's end, and over its start
+        if ws + n <= a[at]:
+            continue
+        with pytest.raises(rocs.RocsError) as e:
+            R.rocs_dca_cross_attn_kv4(d, a["q"], 256, 8, a["cache"], a["table"], 1024, a["kv"], a["off"], 1, 8, 1.0, 0, a["o"], 256, ws, n, stream())
+        assert e.value.status == rocs.ROCS_ERR_INVALID_ARG and "the workspace overlaps" in str(e.value)

@@ -283,3 +283,26 @@ def test_attention_refuses_scales_whose_products_overflow(rocs, h, scale):
     d = rocs.Kv4Desc(40, 64, 8, 32)
     assert rocs._lib_attn4(h, ctypes.byref(d), *{**AT, "scale": scale}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
     assert "2^126" in rocs.rocs_last_error()
+
+
+@pytest.mark.parametrize("change", [      # Qo is 10 rows of 512 bytes, Ko of 256
+    dict(Qo=(3 << 20) + 240), dict(Qo=(4 << 20) - 5104), dict(Ko=(3 << 20) + 240), dict(Ko=(4 << 20) - 2544), dict(Qo=(5 << 20) + 25584),
+    dict(Ko=(5 << 20) - 2544), dict(Qo=(6 << 20) + 32), dict(Ko=6 << 20), dict(Ko=(6 << 20) - 4592, ld_Ko=256), dict(H_q=0, Ko=4 << 20),
+])
+def test_qk_norm_rope_refuses_outputs_over_its_tables(rocs, h, change):
+    a = {**QK, **change}
+    d = rocs.QkDesc(*[a[k] for k in ("rows", "H_q", "H_k", "d_h", "d_rot", "interleaved", "max_pos", "eps", "io")])
+    st = rocs._lib_qk(h, ctypes.byref(d), *[a[k] for k in ("Q", "ld_Q", "K", "ld_K", "gq", "gk", "cs", "pos", "Qo", "ld_Qo", "Ko", "ld_Ko")], None)
+    assert st == rocs.ROCS_ERR_INVALID_ARG and "overlaps the gammas, the angles or the positions" in rocs.rocs_last_error()
+
+
+@pytest.mark.parametrize("at,what", [("past", "input"), ("new", "input"), ("free", "input"), ("table", "output"), ("kv", "output"), ("off", "output"),
+                                     ("slots", "output"), ("pos", "output"), ("used", "output")])
+def test_block_tables_refuses_a_workspace_over_its_tensors(rocs, h, at, what):
+    a = {**TAB, "B_R": 5000, **{k: (i + 1) << 24 for i, k in enumerate(("past", "new", "free", "table", "kv", "off", "slots", "pos", "used"))}}
+    n = ctypes.c_size_t(0)
+    assert rocs._lib_tab_ws(h, 5000, ctypes.byref(n)) == rocs.ROCS_OK and n.value > 16
+    a.update(ws=a[at] - n.value + 16, ws_bytes=n.value)
+    a["ws"] -= a["ws"] % 16
+    assert rocs._lib_tab(h, *a.values(), None) == rocs.ROCS_ERR_INVALID_ARG
+    assert f"the workspace overlaps an {what}" in rocs.rocs_last_error()
