@@ -292,137 +292,139 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
       }
       if (live && part >= 0) p.part_ml[item] = make_float2(m_cur, l);
     }
-  } else if (warp != 7) {
-    // ---------------- producers ----------------
+  } else {
+    // (one instruction for all warps of the warpgroup, in front of the roles)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
-    const int t = threadIdx.x - (warp < 8 ? 128 : 160);     // (warp 11 has nothing to do)
-    constexpr int G = D / KV4_GROUP;
-    const int P = 1 << p.P_log2;
-    const int32_t* table = p.table + (long long)a.r * p.max_blocks;
-    // unit u of this thread: group i = u * PRODUCERS + t of [K: key, group | V: key, group].  A block starts on
-    // a page's or (128 tokens) half page's edge, so a unit's place in its record stays the same.
-    uint4 wd[C::UNITS];
-    uint32_t sc[C::UNITS];
-    int next[C::UNITS], key_in[C::UNITS];
-    uint32_t code_at[C::UNITS], scale_at[C::UNITS];
-    uint32_t piece_bad = 0;
-#pragma unroll
-    for (int u = 0; u < C::UNITS; ++u) {
-      const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
-      const bool has = i < C::ALL;
-      key_in[u] = has ? (i / G) % KT_KEYS : 1 << 30;       // a unit too many lies past every key
-      const int o = key_in[u] & (P - 1);
-      code_at[u] = v * kv4_half_bytes(P, D) + o * (D / 2) + (i % G) * 16;
-      scale_at[u] = v * kv4_half_bytes(P, D) + kv4_codes_bytes(P, D) + (o * G + i % G) * 2;
-    }
-    auto pages = [&](int j) {                       // of block j's units; -1 where there is none
-      const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
-      const int32_t* at = table + (((long long)(b_lo + j) * KT_KEYS) >> p.P_log2);
-#pragma unroll
-      for (int u = 0; u < C::UNITS; ++u) next[u] = key_in[u] < left ? at[key_in[u] >> p.P_log2] : -1;
-    };
-    auto load = [&](int j) {
-      piece_bad = 0;
-      const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
-      const int odd = P > KT_KEYS ? (b_lo + j) & 1 : 0;
-      const uint8_t* head = p.cache + (long long)h * kv4_record_bytes(P, D);
-      const long long stride = (long long)p.Hkv * kv4_record_bytes(P, D);
+    if (warp != 7) {
+      // ---------------- producers ----------------
+      const int t = threadIdx.x - (warp < 8 ? 128 : 160);     // (warp 11 has nothing to do)
+      constexpr int G = D / KV4_GROUP;
+      const int P = 1 << p.P_log2;
+      const int32_t* table = p.table + (long long)a.r * p.max_blocks;
+      // unit u of this thread: group i = u * PRODUCERS + t of [K: key, group | V: key, group].  A block starts on
+      // a page's or (128 tokens) half page's edge, so a unit's place in its record stays the same.
+      uint4 wd[C::UNITS];
+      uint32_t sc[C::UNITS];
+      int next[C::UNITS], key_in[C::UNITS];
+      uint32_t code_at[C::UNITS], scale_at[C::UNITS];
+      uint32_t piece_bad = 0;
 #pragma unroll
       for (int u = 0; u < C::UNITS; ++u) {
-        wd[u] = make_uint4(0, 0, 0, 0);
-        sc[u] = 0;
-        if (key_in[u] < left) {
-          if (next[u] >= 0 && next[u] < p.n_pages) {
-            const uint8_t* at = head + next[u] * stride;
-            wd[u] = *reinterpret_cast<const uint4*>(at + code_at[u] + odd * kv4_codes_bytes(KT_KEYS, D));
-            sc[u] = *reinterpret_cast<const uint16_t*>(at + scale_at[u] + odd * kv4_scales_bytes(KT_KEYS, D));
-          } else {
-            piece_bad |= 1u << (key_in[u] >> 4);
-          }
-        }
+        const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
+        const bool has = i < C::ALL;
+        key_in[u] = has ? (i / G) % KT_KEYS : 1 << 30;       // a unit too many lies past every key
+        const int o = key_in[u] & (P - 1);
+        code_at[u] = v * kv4_half_bytes(P, D) + o * (D / 2) + (i % G) * 16;
+        scale_at[u] = v * kv4_half_bytes(P, D) + kv4_codes_bytes(P, D) + (o * G + i % G) * 2;
       }
-    };
-    if (t < C::PRODUCERS) {
-      pages(0);
-      load(0);
-      pages(1);
-      for (int j = 0; j < n; ++j) {
-        const int st = j % C::STAGES;
-        if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait_sleep(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag, kKtProducerSleepNs)))
-          break;
-        uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
+      auto pages = [&](int j) {                       // of block j's units; -1 where there is none
+        const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
+        const int32_t* at = table + (((long long)(b_lo + j) * KT_KEYS) >> p.P_log2);
+#pragma unroll
+        for (int u = 0; u < C::UNITS; ++u) next[u] = key_in[u] < left ? at[key_in[u] >> p.P_log2] : -1;
+      };
+      auto load = [&](int j) {
+        piece_bad = 0;
+        const int left = j < n ? a.len - (b_lo + j) * KT_KEYS : 0;
+        const int odd = P > KT_KEYS ? (b_lo + j) & 1 : 0;
+        const uint8_t* head = p.cache + (long long)h * kv4_record_bytes(P, D);
+        const long long stride = (long long)p.Hkv * kv4_record_bytes(P, D);
 #pragma unroll
         for (int u = 0; u < C::UNITS; ++u) {
-          const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
-          const int g = i % G;
-          const uint32_t s2 = sc[u] | (sc[u] << 16), c2 = kv4_offset(s2);
-          const uint32_t w[4] = {wd[u].x, wd[u].y, wd[u].z, wd[u].w};
-          if (key_in[u] < KT_KEYS) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
-                                         kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
-              *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(key_in[u], g * 4 + k, C::KV_PANEL)) = e;
+          wd[u] = make_uint4(0, 0, 0, 0);
+          sc[u] = 0;
+          if (key_in[u] < left) {
+            if (next[u] >= 0 && next[u] < p.n_pages) {
+              const uint8_t* at = head + next[u] * stride;
+              wd[u] = *reinterpret_cast<const uint4*>(at + code_at[u] + odd * kv4_codes_bytes(KT_KEYS, D));
+              sc[u] = *reinterpret_cast<const uint16_t*>(at + scale_at[u] + odd * kv4_scales_bytes(KT_KEYS, D));
+            } else {
+              piece_bad |= 1u << (key_in[u] >> 4);
             }
           }
         }
-        if (piece_bad != 0) {
-          atomicOr(&s_bad[j & 7], piece_bad);
-          set_status(p.status, ROCS_ERR_INDEX);
+      };
+      if (t < C::PRODUCERS) {
+        pages(0);
+        load(0);
+        pages(1);
+        for (int j = 0; j < n; ++j) {
+          const int st = j % C::STAGES;
+          if (j >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait_sleep(&kv_empty[st], ((j / C::STAGES) - 1) & 1, p.status, &abort_flag, kKtProducerSleepNs)))
+            break;
+          uint8_t* kv = sKV + st * 2 * C::KV_BYTES;
+#pragma unroll
+          for (int u = 0; u < C::UNITS; ++u) {
+            const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
+            const int g = i % G;
+            const uint32_t s2 = sc[u] | (sc[u] << 16), c2 = kv4_offset(s2);
+            const uint32_t w[4] = {wd[u].x, wd[u].y, wd[u].z, wd[u].w};
+            if (key_in[u] < KT_KEYS) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 e = make_uint4(kv4_fma2(kv4_pair(w[k]), s2, c2), kv4_fma2(kv4_pair(w[k] >> 4), s2, c2),
+                                           kv4_fma2(kv4_pair(w[k] >> 8), s2, c2), kv4_fma2(kv4_pair(w[k] >> 12), s2, c2));
+                *reinterpret_cast<uint4*>(kv + v * C::KV_BYTES + kt_unit<D>(key_in[u], g * 4 + k, C::KV_PANEL)) = e;
+              }
+            }
+          }
+          if (piece_bad != 0) {
+            atomicOr(&s_bad[j & 7], piece_bad);
+            set_status(p.status, ROCS_ERR_INDEX);
+          }
+          fence_proxy_async_smem();
+          warp_arrive(&kv_full[st]);
+          // after the fence, which would wait for loads in front of it
+          load(j + 1);
+          pages(j + 2);
         }
-        fence_proxy_async_smem();
-        warp_arrive(&kv_full[st]);
-        // after the fence, which would wait for loads in front of it
-        load(j + 1);
-        pages(j + 2);
       }
-    }
-  } else {
-    // ---------------- MMA issuer: the whole warp, so that its operands stay uniform ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONTROL));
-    const uint64_t qd = sdesc(smem_u32(sQ), C::SBO, C::SW), kd = sdesc(smem_u32(sKV), C::SBO, C::SW);
-    const bool one = elect_one();
-    auto issue_s = [&](int j) -> bool {
-      const int st = j % C::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
-      tc_fence_after();
+    } else {
+      // ---------------- MMA issuer: the whole warp, so that its operands stay uniform ----------------
+      const uint64_t qd = sdesc(smem_u32(sQ), C::SBO, C::SW), kd = sdesc(smem_u32(sKV), C::SBO, C::SW);
+      const bool one = elect_one();
+      auto issue_s = [&](int j) -> bool {
+        const int st = j % C::STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(&kv_full[st], (j / C::STAGES) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
+        tc_fence_after();
+        if (one) {
+          const uint64_t k = kd + st * (2 * C::KV_BYTES >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_mma_ss(s_tmem + (j & 1) * KT_KEYS, qd + (((ks >> 2) * C::Q_PANEL + (ks & 3) * 32) >> 4),
+                      k + (((ks >> 2) * C::KV_PANEL + (ks & 3) * 32) >> 4), IDESC_S, ks > 0 ? 1u : 0u);
+          tc_commit(&s_full[j & 1]);
+        }
+        return true;
+      };
+      auto issue_pv = [&](int j) -> bool {
+        const int st = j % C::STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
+        tc_fence_after();
+        if (one) {
+          const uint64_t v = kd + st * (2 * C::KV_BYTES >> 4) + (C::KV_BYTES >> 4);
+          const uint32_t acc = j > 0 ? 1u : 0u;
+#pragma unroll
+          for (int pn = 0; pn < C::PANELS; ++pn)
+#pragma unroll
+            for (int ks = 0; ks < KT_KEYS / 16; ++ks)
+              tc_mma_ts(o_tmem + pn * 64, s_tmem + (j & 1) * KT_KEYS + ks * 8,
+                        v + ((pn * C::KV_PANEL + ks * 16 * C::ROWB) >> 4), IDESC_O, ks > 0 ? 1u : acc);
+          tc_commit(&kv_empty[st]);
+          tc_commit(&pv_done[j & 1]);
+        }
+        return true;
+      };
+      bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(&q_full, 0, p.status, &abort_flag, kKtIssuerSleepNs));
+      if (ok && n > 0) ok = issue_s(0) && (n < 2 || issue_s(1));
+      for (int j = 0; ok && j < n; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
+      __syncwarp();
       if (one) {
-        const uint64_t k = kd + st * (2 * C::KV_BYTES >> 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_ss(s_tmem + (j & 1) * KT_KEYS, qd + (((ks >> 2) * C::Q_PANEL + (ks & 3) * 32) >> 4),
-                    k + (((ks >> 2) * C::KV_PANEL + (ks & 3) * 32) >> 4), IDESC_S, ks > 0 ? 1u : 0u);
-        tc_commit(&s_full[j & 1]);
+        tc_commit(&drain);
+        mbar_wait(&drain, 0, p.status, nullptr);
       }
-      return true;
-    };
-    auto issue_pv = [&](int j) -> bool {
-      const int st = j % C::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&p_full[j & 1], (j >> 1) & 1, p.status, &abort_flag, kKtIssuerSleepNs))) return false;
-      tc_fence_after();
-      if (one) {
-        const uint64_t v = kd + st * (2 * C::KV_BYTES >> 4) + (C::KV_BYTES >> 4);
-        const uint32_t acc = j > 0 ? 1u : 0u;
-#pragma unroll
-        for (int pn = 0; pn < C::PANELS; ++pn)
-#pragma unroll
-          for (int ks = 0; ks < KT_KEYS / 16; ++ks)
-            tc_mma_ts(o_tmem + pn * 64, s_tmem + (j & 1) * KT_KEYS + ks * 8,
-                      v + ((pn * C::KV_PANEL + ks * 16 * C::ROWB) >> 4), IDESC_O, ks > 0 ? 1u : acc);
-        tc_commit(&kv_empty[st]);
-        tc_commit(&pv_done[j & 1]);
-      }
-      return true;
-    };
-    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(&q_full, 0, p.status, &abort_flag, kKtIssuerSleepNs));
-    if (ok && n > 0) ok = issue_s(0) && (n < 2 || issue_s(1));
-    for (int j = 0; ok && j < n; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
-    __syncwarp();
-    if (one) {
-      tc_commit(&drain);
-      mbar_wait(&drain, 0, p.status, nullptr);
+      __syncwarp();
     }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
