@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, KtCfg<D>::CTAS) attn_kv4_tc
       for (int u = 0; u < C::UNITS; ++u) {
         const int i = u * C::PRODUCERS + t, v = i >= KT_KEYS * G;
         const bool has = i < C::ALL;
-        key_in[u] = has ? (i / G) % KT_KEYS : 1 << 30;       // a unit too many lies past every key
+        key_in[u] = has ? (i / G) % KT_KEYS : 0x7FFFFFFF;   // a unit too many lies past every key
         const int o = key_in[u] & (P - 1);
         code_at[u] = v * kv4_half_bytes(P, D) + o * (D / 2) + (i % G) * 16;
         scale_at[u] = v * kv4_half_bytes(P, D) + kv4_codes_bytes(P, D) + (o * G + i % G) * 2;

@@ -1,12 +1,16 @@
 """The 4-bit history cache's calls where they go wrong most easily, against the float64 oracle: pages that run
-out between requests of all sizes, and weights that round alike."""
+out between requests of all sizes, scores and weights of all sizes, the forms that only large calls take, mixed
+batches, and the calls together with the encoder.  Tolerances are those of test_gpu_kv_cache.py unless a test says
+otherwise."""
 import math
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import kv_cache as KC
-from tests.gpu_util import stream
+from tests import test_gpu_kv_cache as base
+from tests.gpu_util import check_bf16, dev, dev_i32, host, stream
 from tests.test_gpu_kv_cache import Cached, R, check_tables, close, run_tables, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -160,3 +164,34 @@ def test_attention_refuses_a_workspace_over_its_tensors(R, at, inside):  # noqa:
         with pytest.raises(rocs.RocsError) as e:
             R.rocs_dca_cross_attn_kv4(d, a["q"], 256, 8, a["cache"], a["table"], 1024, a["kv"], a["off"], 1, 8, 1.0, 0, a["o"], 256, ws, n, stream())
         assert e.value.status == rocs.ROCS_ERR_INVALID_ARG and "the workspace overlaps" in str(e.value)
+
+
+@pytest.mark.parametrize("rows", [1, 64])
+def test_attention_of_a_history_past_a_billion_tokens(R, rows):  # noqa: F811
+    """Its pages are three pages over and over, so the result is that of three pages' keys, each weighed by how often it comes.
+    A block has up to 2^30 / 444 keys, 16 or more of them in each addition to a sum that may lose 2^-23 of it: 2^-23 * 2^18 of mag
+    beside the usual tolerance."""
+    from request_candidate_sharing_b200 import rocs
+    page, d = 128, 32
+    c = Cached(34, [rows], [3 * page], 1, 1, d, page)
+    g = np.random.default_rng(1)
+    length = 2 ** 30 + 5 * page + 77
+    blocks = -(-length // page)
+    table = c.table[0, g.choice(3, blocks, p=[0.5, 0.3, 0.2])]
+    desc = rocs.Kv4Desc(c.n_pages, page, 1, d)
+    q, cache, t = torch.from_numpy(c.Q).to(torch.bfloat16).cuda(), torch.from_numpy(c.cache).cuda(), torch.from_numpy(table).cuda()
+    kv, off = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([length], [0, rows]))
+    out = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    n = R.rocs_dca_cross_attn_kv4_workspace(desc, 1, 1, rows, blocks)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    R.rocs_dca_cross_attn_kv4(desc, q, d, 1, cache, t, blocks, kv, off, 1, rows, 0.2, 0, out, d, ws, n, stream())
+    assert status(R) == 0
+    times = np.array([(table[:-1] == p).sum() for p in c.table[0, :3]])[:, None] + (np.arange(page) < 77) * (table[-1] == c.table[0, :3])[:, None]
+    assert times.sum() == length
+    k, v = (x[c.table[0, :3], 0].reshape(-1, d) for x in (c.K, c.V))
+    s = c.Q[:, 0] @ k.T * 0.2
+    w = np.exp(s - s.max(-1, keepdims=True)) * times.reshape(-1)
+    w /= w.sum(-1, keepdims=True)
+    want, mag = w @ v, w @ np.abs(v)
+    got = host(out)
+    assert (np.abs(got - want) <= 2.0 ** -8 * (mag + np.abs(want)) * (1 + 2.0 ** -8) + (2.0 ** -10 + 2.0 ** -5) * mag).all()
