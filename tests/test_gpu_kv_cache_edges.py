@@ -195,3 +195,155 @@ def test_attention_of_a_history_past_a_billion_tokens(R, rows):  # noqa: F811
     want, mag = w @ v, w @ np.abs(v)
     got = host(out)
     assert (np.abs(got - want) <= 2.0 ** -8 * (mag + np.abs(want)) * (1 + 2.0 ** -8) + (2.0 ** -10 + 2.0 ** -5) * mag).all()
+
+
+# ---- forms that only large calls take ----------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,Hq,Hk,d,rot,inter,io", [
+    # several items a warp; heads in two units, the second one partly filled; bf16 whole heads, both pairings
+    (5003, 12, 3, 32, 32, 0, 1), (5003, 12, 3, 32, 32, 1, 1), (5003, 5, 7, 64, 64, 0, 1), (5003, 5, 7, 64, 64, 1, 1), (2003, 3, 3, 128, 128, 0, 1),
+    (2003, 3, 3, 128, 128, 1, 1), (3601, 1, 1, 256, 256, 0, 1), (5003, 17, 0, 16, 16, 1, 1),
+    # parts of heads, and fp32
+    (5003, 5, 7, 64, 32, 1, 1), (5003, 3, 2, 80, 48, 1, 1), (5003, 5, 7, 64, 64, 1, 0), (5003, 3, 2, 96, 64, 1, 0), (5003, 3, 2, 96, 64, 0, 0),
+])
+def test_qk_norm_rope_of_many_rows(R, rows, Hq, Hk, d, rot, inter, io):  # noqa: F811
+    base.test_qk_norm_rope(R, rows, Hq, Hk, d, rot, inter, io, 1)
+
+
+@pytest.mark.parametrize("rows,H,page,d", [(30011, 5, 16, 32), (120001, 1, 64, 32), (14209, 8, 128, 32), (30011, 5, 32, 64), (15007, 5, 16, 128)])
+def test_append_and_gather_of_many_rows(R, rows, H, page, d):  # noqa: F811
+    """Two row sets a warp, with skipped rows and an odd end."""
+    base.test_append_and_gather(R, rows, H, page, d)
+
+
+@pytest.mark.parametrize("B,H,share,d,causal", [
+    (300, 8, 1, 32, 0), (300, 8, 1, 32, 1), (700, 5, 1, 32, 0), (250, 8, 2, 64, 1), (450, 5, 1, 128, 0),         # two warps a head
+    (1300, 3, 1, 32, 0), (700, 8, 1, 32, 0), (700, 8, 1, 32, 1), (1000, 5, 2, 32, 0), (1000, 5, 1, 64, 1), (800, 6, 1, 128, 0),      # one
+    (8200, 3, 1, 32, 0), (8200, 3, 1, 32, 1), (8200, 5, 1, 64, 0),                 # one, past the list
+])
+def test_attention_of_many_heads_a_block(R, B, H, share, d, causal):  # noqa: F811
+    """Few rows of many requests: a block takes several neighbouring heads, the last block of a tile fewer."""
+    g = np.random.default_rng(B + H)
+    lens = g.integers(0, 300 if B < 8000 else 40, B)
+    lens[::7] = g.integers(0, 3, len(lens[::7]))
+    c = Cached(35, g.integers(0, 3, B), lens, H, share, d, 16, pad_rows=3)
+    got = c.run(R, d ** -0.5, causal)
+    assert status(R) == 0
+    n = int(c.offsets[-1])
+    want, mag = c.want(d ** -0.5, causal)
+    close(got[:n], want[:n], mag[:n])
+    assert (got[n:] == 9).all()
+
+
+@pytest.mark.parametrize("counts,pad", [([1] * 480 + [200] * 8, 5), ([0] * 200 + [300, 0, 0, 180, 7] + [0] * 100, 1200), ([1, 1, 700, 1] * 6, 0)])
+@pytest.mark.parametrize("d,share", [(32, 1), (64, 2), (128, 1)])
+def test_attention_of_mixed_and_padded_batches(R, counts, pad, d, share):  # noqa: F811
+    """Single rows and bursts in one call, and a captured step's empty requests and padded rows."""
+    g = np.random.default_rng(len(counts))
+    c = Cached(36, counts, g.integers(0, 700, len(counts)), 1, share, d, 64, pad_rows=pad)
+    got = c.run(R, d ** -0.5, 0)
+    assert status(R) == 0
+    n = int(c.offsets[-1])
+    want, mag = c.want(d ** -0.5, 0)
+    close(got[:n], want[:n], mag[:n])
+    assert (got[n:] == 9).all()
+
+
+@pytest.mark.parametrize("q,B,H,lens", [(40, 300, 2, 40), (1, 600, 8, 40), (1, 5, 1, 9000), (3, 40, 1, 5000), (50, 3, 1, 5000)])
+def test_attention_offsets_back_and_forth_write_nothing_from_a_list(R, q, B, H, lens):  # noqa: F811
+    """Listed and split forms: requests that all claim every row would not fit the list, so none is done."""
+    c = Cached(37, [q] * B, [lens] * B if B > 5 else [lens, 0, 70, 0, 300][:B], H, 1, 32, 16)
+    off = np.where(np.arange(B + 1) % 2 == 0, 0, c.rows)
+    got = c.run(R, 0.2, 0, offsets=off)
+    assert status(R) == 5 and (got == 9).all()
+
+
+# ---- the calls together ----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("B,H,share,d,page", [(4, 2, 2, 64, 16), (3, 2, 1, 32, 64)])
+def test_serving_steps_norm_and_rotate_by_their_positions(R, B, H, share, d, page):  # noqa: F811
+    """The queries and keys that a step's attention works on, against the oracle's norm and rotation of what was
+    handed in, at each event's place in its history."""
+    g = np.random.default_rng(40 + B)
+    rows, Hq = 96, H * share
+    st = base.Step(R, B, H, share, d, page, 8, 60, rows)
+    gamma, cs = st.gamma.cpu().numpy(), st.cs.cpu().numpy()
+    past = np.zeros(B, int)
+    hist = [[] for _ in range(B)]
+    for new in (g.integers(10, 25, B), np.ones(B, int), np.array([1, 0, 17] + [3] * (B - 3))):
+        x = base.bf16(g.normal(size=(rows, st.width)))
+        st.new.copy_(dev_i32(new))
+        st.qkv.copy_(x.cuda())
+        st.calls()
+        assert status(R) == 0
+        pos = np.concatenate([p + np.arange(n) for p, n in zip(past, new)] + [np.full(rows - new.sum(), -1)])
+        assert np.array_equal(st.pos.cpu().numpy(), pos)
+        was, qkv, n = x.double().numpy(), host(st.qkv), int(new.sum())
+        for at, heads in ((0, Hq), (Hq * d, H)):
+            y, mag = KC.qk_norm_rope(was[:, at:at + heads * d].reshape(rows, heads, d), gamma, 1e-6, cs, pos, 0)
+            got = qkv[:, at:at + heads * d].reshape(rows, heads, d)
+            tol = (16 * 2.0 ** -24 * mag + 2.0 ** -8 * np.abs(y)) * (1 + 2.0 ** -8)
+            assert (np.abs(got - y) <= tol)[:n].all() and (got[n:] == was[n:, at:at + heads * d].reshape(-1, heads, d)).all()
+        assert np.array_equal(qkv[:, (Hq + H) * d:], was[:, (Hq + H) * d:])            # the values are not touched
+        want, mag = base.reference_step(hist, new, qkv, st.off.cpu().numpy(), H, share, d, page, None, None)
+        close(host(st.out)[:n].reshape(n, Hq, d), want, mag)
+        past += new
+        st.past.copy_(st.kv)
+        used = int(st.used.item())
+        st.free.copy_(torch.cat([st.free[used:], st.free[:used]]))
+
+
+def test_encoded_histories_in_the_cache(R):  # noqa: F811
+    """The encoder's candidate-side keys and values of ragged histories (padded to L rows a request) go to the cache by the slots
+    of the block tables, candidates attend to them there, and they come back for the dense attention."""
+    import synth
+    from request_candidate_sharing_b200 import rocs
+    lengths, counts = np.array([37, 64, 1, 50]), np.array([5, 0, 70, 33])
+    case = synth.model_cfg4(B_R=4, counts=list(counts))
+    a, B, page = case.dca, 4, 16
+    L, d, H = a.L, a.d, a.H
+    dh = d // H
+    assert L >= 64 and dh == 64
+    W, x = synth.model_weights(case), synth.model_inputs(case)
+    Wd = {k: dev(v, torch.float32 if "ln." in k else torch.bfloat16) for k, v in W.items()}
+    desc = rocs.DcaDesc(B, L, d, H, a.layers)
+    nb = R.rocs_dca_encode_workspace(desc)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    S, KV = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((a.layers, B, L, d), (a.layers, 4, B, L, d)))
+    n_new = dev_i32(lengths)
+    R.rocs_dca_encode(desc, dev(x["H"]), [rocs.dca_layer_weights(Wd, l) for l in range(a.layers)], S, KV, ws, nb, stream(), lengths=n_new)
+    K, V = KV[-1, 2], KV[-1, 3]
+    # slots of the compact rows, laid out by the padded rows' places: -1 past each history's end
+    total, n_pages, blocks = int(lengths.sum()), 20, L // page + 1
+    table = torch.full((B, blocks), -1, dtype=torch.int32, device="cuda")
+    kv, off, used, pos = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in (B, B + 1, 1, total))
+    slots = torch.zeros(total, dtype=torch.int64, device="cuda")
+    free = torch.randperm(n_pages, generator=torch.Generator().manual_seed(3)).int().cuda()
+    R.rocs_kv_block_tables(None, n_new, B, page, free, n_pages, n_pages, table, blocks, kv, off, slots, pos, total, used, None, 0, stream())
+    padded = torch.full((B, L), -1, dtype=torch.int64, device="cuda")
+    padded[torch.arange(L, device="cuda") < n_new[:, None]] = slots
+    cdesc = rocs.Kv4Desc(n_pages, page, H, dh)
+    cache = torch.zeros(n_pages, H, KC.record_bytes(page, dh), dtype=torch.uint8, device="cuda")
+    R.rocs_kv4_append(cdesc, K, d, V, d, padded, B * L, cache, stream())
+    assert status(R) == 0
+    real = host(padded.reshape(-1)) >= 0
+    want_cache = KC.append(np.zeros(cache.shape, np.uint8), page, host(K).reshape(-1, H, dh)[real], host(V).reshape(-1, H, dh)[real], slots.cpu().numpy())
+    assert np.array_equal(cache.cpu().numpy(), want_cache)
+    # candidates over the cache
+    rows = int(counts.sum())
+    Q = base.bf16(np.random.default_rng(8).normal(size=(rows, d)))
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    out = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    n = R.rocs_dca_cross_attn_kv4_workspace(cdesc, H, B, rows, blocks)
+    aws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    Qd, offd = Q.cuda(), dev_i32(offsets)
+    R.rocs_dca_cross_attn_kv4(cdesc, Qd, d, H, cache, table, blocks, kv, offd, B, rows, dh ** -0.5, 0, out, d, aws, n, stream())
+    assert status(R) == 0
+    want, mag = KC.attention(Q.double().numpy().reshape(rows, H, dh), H, *KC.values(want_cache, page, dh), table.cpu().numpy(), lengths, offsets, page,
+                             dh ** -0.5, 0)
+    close(host(out).reshape(rows, H, dh), want, mag)
+    # and back, for the dense attention over the same values
+    Kb, Vb = torch.zeros_like(K), torch.zeros_like(V)
+    R.rocs_kv4_gather(cdesc, cache, padded, B * L, Kb, d, Vb, d, stream())
+    dense = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    R.rocs_dca_cross_attn(Qd, Kb, Vb, offd, B, rows, L, H, dh, dh ** -0.5, dense, d, rocs.ROCS_BF16, stream(), kv_len=kv)
+    assert status(R) == 0
+    check_bf16(host(dense), want.reshape(rows, d), out_bf16=True, what="dense attention over what the cache gave back")
