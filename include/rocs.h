@@ -319,7 +319,13 @@ rocs_status rocs_dca_cross_attn_unsorted(rocs_handle_t handle, const void* Q, co
  *   rocs_qk_norm_rope        head norms and position rotation of the new queries and keys
  *   rocs_kv4_append          new keys and values into their slots
  *   rocs_dca_cross_attn_kv4  query rows (candidates, or the new events) against the cached history
- * rocs_kv4_gather reads rows back as bf16 (for the dense rocs_dca_cross_attn, or to move pages).
+ * rocs_kv4_gather reads rows back as bf16, from whatever slots it is given, in their order.
+ * Candidates over encoded histories: rocs_dca_encode's keys and values have L rows a request, so append
+ * (and gather, for the dense rocs_dca_cross_attn) takes slots [B_R, L]: those of row_offsets[r] + j at
+ * (r, j), and -1 from lengths[r] on.  That encoder is not causal: after a new event all of a history's
+ * keys and values are others, and are appended anew (past_len NULL, the old pages back on the free list).
+ * Histories that grow by appending need keys that later events do not change (causal = 1, positions by
+ * rocs_qk_norm_rope): an encoder of the caller's, of the linears and these calls.
  * [REV] and [SUM] have no counterpart of the cache; the grouped attention is that of a9.
  *
  * Storage.  A cache of n_pages pages, page_size tokens each, is one buffer [n_pages, H_kv, record]
@@ -362,6 +368,10 @@ rocs_status rocs_kv4_cache_bytes(rocs_handle_t handle, const rocs_kv4_desc* desc
  * new rows that sum to more than `rows` set it too (those beyond are not written, nor the table entries
  * of pages that begin in them).  A page outside [0, n_pages), in the table or the free list, gives its
  * rows -1 and sets ROCS_ERR_INDEX.
+ * A row whose position is -1 has no result in this step, whatever the calls behind write for it: norm and
+ * rotation, append and gather leave it out, but the attention knows no positions, and with causal = 1 takes
+ * a refused request's rows (which row_offsets counts) for the last new_len of the tokens that it holds.
+ * Read the status, or drop those rows, before the step's results are used.
  * The outputs may not overlap the inputs or one another, nor the workspace any of them.
  * slots and positions 16-byte aligned.  workspace: rocs_kv_block_tables_workspace bytes (0 up to 2048
  * requests), 16-byte aligned, for this call alone until its work is done.  Limits: 1 <= B_R <= 2^24;
@@ -423,7 +433,9 @@ rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, con
  *     0 .. kv_len[r] - 1 (0 <= kv_len[r] <= max_blocks * page_size); entries past its last page are not
  *     read.
  *   causal = 0: every row sees all of its request's keys.  causal = 1: the request's n_r rows are its
- *     last n_r tokens, so row i (from 0) sees the keys j <= kv_len[r] - n_r + i.
+ *     last n_r tokens, so row i (from 0) sees the keys j <= kv_len[r] - n_r + i.  That the tokens are
+ *     cached is the caller's word: rows whose position rocs_kv_block_tables gave as -1 are not, and
+ *     what is written for them is no result.
  *   O [rows, H_q * d_h] bf16, row stride ld_O: softmax(q k^T * scale) v; a row that sees no key is 0.
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights enter the second product as
  * bf16.  Offsets that decrease or leave [0, rows] set ROCS_ERR_INDEX, a kv_len outside its range

@@ -291,6 +291,43 @@ def test_serving_steps_norm_and_rotate_by_their_positions(R, B, H, share, d, pag
         st.free.copy_(torch.cat([st.free[used:], st.free[:used]]))
 
 
+def test_serving_step_with_a_refused_request(R):  # noqa: F811
+    """A burst finds too few pages: its rows have position -1, it keeps its history, the others are served, and what the causal
+    attention writes for it is what the header says, its plain queries against the tokens it holds, shifted."""
+    B, H, share, d, page, rows = 3, 2, 1, 32, 16, 96
+    g = np.random.default_rng(50)
+    st = base.Step(R, B, H, share, d, page, 8, 60, rows)
+    hist = [[] for _ in range(B)]
+    for new, n_free in (([10, 20, 5], 60), ([3, 40, 12], 1)):
+        new = np.array(new)
+        x = base.bf16(g.normal(size=(rows, st.width)))
+        st.new.copy_(dev_i32(new))
+        st.qkv.copy_(x.cuda())
+        st.free = st.free[:n_free].contiguous()
+        st.calls()
+        assert status(R) == (0 if n_free > 1 else 7)
+        qkv, off, out = host(st.qkv), st.off.cpu().numpy(), host(st.out).reshape(rows, H, d)
+        if n_free > 1:
+            want, mag = base.reference_step(hist, new, qkv, off, H, share, d, page, None, None)
+            close(out[:35], want, mag)
+            used = int(st.used.item())
+            st.past.copy_(st.kv)
+            st.free = st.free[used:].contiguous()
+    assert st.kv.tolist() == [13, 20, 17] and off.tolist() == [0, 3, 43, 55] and st.used.item() == 1
+    pos = st.pos.cpu().numpy()
+    assert pos[:3].tolist() == [10, 11, 12] and (pos[3:43] == -1).all() and pos[43:55].tolist() == list(range(5, 17)) and (pos[55:] == -1).all()
+    assert (qkv[3:43] == x.double().numpy()[3:43]).all()
+    # the others, as without it
+    served = np.r_[0:3, 43:55]
+    want, mag = base.reference_step([hist[0], hist[2]], np.array([3, 12]), qkv[served], np.array([0, 3, 15]), H, share, d, page, None, None)
+    close(out[served], want, mag)
+    old = np.concatenate(hist[1])
+    kv = [KC.dequantize(*KC.quantize(y)).transpose(1, 0, 2)[None] for y in (old[:, H:2 * H], old[:, 2 * H:])]
+    want, mag = KC.attention(qkv[3:43, :H * d].reshape(40, H, d), H, *kv, np.zeros((1, 1), int), [20], [0, 40], 20, d ** -0.5, 1)
+    close(out[3:43], want, mag)
+    assert (out[3:23] == 0).all() and (out[55:] == 9).all()
+
+
 def test_encoded_histories_in_the_cache(R):  # noqa: F811
     """The encoder's candidate-side keys and values of ragged histories (padded to L rows a request) go to the cache by the slots
     of the block tables, candidates attend to them there, and they come back for the dense attention."""
