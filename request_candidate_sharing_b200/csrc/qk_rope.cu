@@ -122,6 +122,10 @@ __device__ __forceinline__ uint64_t qk_fma(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+// Means of squares that fp32 holds as exactly as any; heads beyond are scaled by a power of two, which changes
+// nothing else of y.
+constexpr float kQkSmall = 0x1p-100f, kQkLarge = 0x1p+120f;
+
 // T lanes a head (a power of two, T * 8 >= d).  HALVES: pairs are (t, t + d_rot / 2).  FULL: d = 8 T and
 // all of it turns, the usual case, without predicates.  N items a warp.
 template <typename E, int T, bool HALVES, bool FULL, int N>
@@ -194,12 +198,26 @@ __global__ void __launch_bounds__(256, N == 1 ? 6 : N == 4 ? 3 : 4) qk_norm_rope
     float x[4], y[4];
     raw[i].template get<HALVES>(x, y);
     uint64_t xp[2] = {qk_pk(x[0], x[1]), qk_pk(x[2], x[3])}, yp[2] = {qk_pk(y[0], y[1]), qk_pk(y[2], y[3])};
-    float s0, s1;
-    qk_un(qk_fma(yp[1], yp[1], qk_fma(yp[0], yp[0], qk_fma(xp[1], xp[1], qk_mul(xp[0], xp[0])))), s0, s1);
-    float ss = s0 + s1;
+    auto squares = [&]() {               // of the head
+      float s0, s1;
+      qk_un(qk_fma(yp[1], yp[1], qk_fma(yp[0], yp[0], qk_fma(xp[1], xp[1], qk_mul(xp[0], xp[0])))), s0, s1);
+      float ss = s0 + s1;
 #pragma unroll
-    for (int o = 1; o < T; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rn = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+      for (int o = 1; o < T; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      return ss;
+    };
+    float mean = fmaf(squares(), p.inv_d, p.eps);
+    if (__any_sync(0xffffffffu, !(mean > kQkSmall && mean < kQkLarge))) {
+      const float k = mean <= kQkSmall ? 0x1p+100f : mean < kQkLarge ? 1.0f : 0x1p-70f;
+      const uint64_t kp = qk_pk(k, k);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        xp[j] = qk_mul(xp[j], kp);
+        yp[j] = qk_mul(yp[j], kp);
+      }
+      mean = fmaf(squares(), p.inv_d, p.eps * k * k);
+    }
+    const float rn = rsqrtf(mean);
     const uint64_t rp = qk_pk(rn, rn);
     const float c[4] = {cv[i].x, cv[i].y, cv[i].z, cv[i].w}, s[4] = {sv[i].x, sv[i].y, sv[i].z, sv[i].w};
 #pragma unroll

@@ -257,6 +257,27 @@ def test_attention_offsets_back_and_forth_write_nothing_from_a_list(R, q, B, H, 
     assert status(R) == 5 and (got == 9).all()
 
 
+@pytest.mark.parametrize("rows", [70, 5003])
+@pytest.mark.parametrize("d,rot,inter,io", [(32, 32, 0, 1), (64, 32, 1, 1), (128, 128, 0, 0), (80, 48, 1, 0)])
+def test_qk_norm_rope_of_heads_of_all_sizes(R, rows, d, rot, inter, io):  # noqa: F811
+    """Heads whose squares leave fp32's range at either end lie beside common ones; eps is 0 or counts only for the smallest."""
+    from request_candidate_sharing_b200 import rocs
+    g = np.random.default_rng(rows + d)
+    dt, H = torch.bfloat16 if io else torch.float32, 3
+    size = 2.0 ** np.array([0, 124, -120, 63, -66, 90, -50, 10, 60, -130])
+    buf = torch.from_numpy((np.clip(g.normal(size=(rows, H, d)), -6, 6) * size[np.arange(rows * H).reshape(rows, H, 1) % 10]).astype(np.float32)).to(dt)
+    x, pos, cs = buf.double().numpy(), g.integers(0, 50, rows), KC.angles(50, rot)
+    t, post, cst = buf.reshape(rows, -1).cuda(), dev_i32(pos), torch.from_numpy(cs).cuda()
+    for eps in (0.0, 2.0 ** -110):
+        out = torch.zeros_like(t)
+        desc = rocs.QkDesc(rows, H, 0, d, rot, inter, 50, eps, io)
+        R.rocs_qk_norm_rope(desc, t, H * d, None, 0, None, None, cst, post, out, H * d, None, 0, stream())
+        assert status(R) == 0
+        y, mag = KC.qk_norm_rope(x, None, eps, cs, pos, inter)
+        tol = 16 * 2.0 ** -24 * mag + (2.0 ** -8 * np.abs(y) if io else 0)
+        assert (np.abs(host(out).reshape(rows, H, d) - y) <= tol * (1 + 2.0 ** -8) + 1e-30).all()
+
+
 # ---- the calls together ----------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("B,H,share,d,page", [(4, 2, 2, 64, 16), (3, 2, 1, 32, 64)])
 def test_serving_steps_norm_and_rotate_by_their_positions(R, B, H, share, d, page):  # noqa: F811
