@@ -932,6 +932,8 @@ extern "C" rocs_status rocs_kv_block_tables(rocs_handle_t h, const int32_t* past
                "%s: max_blocks=%d out of range", who, max_blocks);
   ROCS_REQUIRE(rows >= 0 && rows < 2147483647LL && (rows == 0 || (slots && positions)), "%s: bad rows", who);
   ROCS_REQUIRE(aligned16(slots) && aligned16(positions), "%s: slots and positions must be 16-byte aligned", who);
+  ROCS_REQUIRE((((uintptr_t)past_len | (uintptr_t)new_len | (uintptr_t)free_pages | (uintptr_t)block_table |
+                 (uintptr_t)kv_len | (uintptr_t)row_offsets | (uintptr_t)pages_used) & 3) == 0, "%s: misaligned", who);
   const void* out[] = {block_table, kv_len, row_offsets, slots, positions, pages_used};
   const size_t n_out[] = {(size_t)B_R * max_blocks * 4, (size_t)B_R * 4, (size_t)B_R * 4 + 4, (size_t)rows * 8,
                           (size_t)rows * 4, 4};

@@ -306,3 +306,9 @@ def test_block_tables_refuses_a_workspace_over_its_tensors(rocs, h, at, what):
     a["ws"] -= a["ws"] % 16
     assert rocs._lib_tab(h, *a.values(), None) == rocs.ROCS_ERR_INVALID_ARG
     assert f"the workspace overlaps an {what}" in rocs.rocs_last_error()
+
+
+@pytest.mark.parametrize("at", ["past", "new", "free", "table", "kv", "off", "used"])
+def test_block_tables_refuses_misaligned_tensors(rocs, h, at):
+    assert rocs._lib_tab(h, *{**TAB, at: TAB[at] + 2}.values(), None) == rocs.ROCS_ERR_INVALID_ARG
+    assert "misaligned" in rocs.rocs_last_error()
