@@ -202,7 +202,6 @@ __global__ void __launch_bounds__(KA_WARPS * 32) attn_kv4_kernel(const KaParams 
     }
   }
   int next_page = page_of(c_issue);
-  if (st_issue == C::STAGES) st_issue = 0;
   int st = 0;
   uint32_t phase = 0;
   bool alive = true;
