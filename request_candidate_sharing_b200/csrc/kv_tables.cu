@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_sum_kernel(const TabPar
 
 // Places the pages of the requests from the first chunk on in which the free list runs out, chunk after chunk,
 // and writes for those requests what tab_owner_writes does; returns the entries taken.  For one whole block.
-// 5 us a chunk: 40000 requests that all get nothing take 0.39 ms, where 40000 that fit take 26 us.
-__device__ __noinline__ long long tab_place_chunks(const TabParams& p) {
+// 5 us a chunk: 40000 requests that all get nothing take 0.37 ms, where 40000 that fit take 26 us.
+__device__ __forceinline__ long long tab_place_chunks(const TabParams& p) {
   __shared__ int32_t s_need[kTabThreads], s_at[kTabThreads];
   __shared__ unsigned s_taken;
   const int chunks = gridDim.x;
