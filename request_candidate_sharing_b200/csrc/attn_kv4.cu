@@ -24,9 +24,10 @@
 // The cache's bytes would be the bound, but turning codes into operands takes as many issue slots: for
 // three histories of 351531 tokens together (8 heads of 128, shared by four query heads) 104 us, of which 62 us are
 // the bytes at the measured copy rate, with the integer pipe 58% busy and 2.3 instructions a cycle; for
-// 512 single queries against histories of 567 keys on average (8 heads of 32) 35 us, of which 13 us are the
+// 512 single queries against histories of 567 keys on average (8 heads of 32) 36 us, of which 13 us are the
 // bytes, 3 the list and the rest the start, the longest histories and the end.  The same calls on the
 // 128-row kernel took three to four times as long.
+// Weights enter the product as bf16 (two bf16 numbers a weight would take 113 and 39 us), and their sum is of those.
 #include <float.h>
 
 #include <type_traits>
@@ -710,7 +711,8 @@ KaPlan ka_plan(const rocs_context* ctx, const rocs_kv4_desc& d, int H_q, int B_R
   if (rows == 0) return k;
   const int share = H_q / d.H_kv;
   const long long packed = rows * share;
-  // as many packed rows per tile as a request has on average
+  // as many packed rows per tile as a request has on average (all that the host knows): right for requests that
+  // are alike.  480 single rows with 32 bursts of 500 take 167 us in one call and 82 in two.
   const double avg = (double)packed / B_R;
   k.NT = avg <= 8 ? 1 : avg <= 16 ? 2 : avg <= kTcRows ? (d.d_h == 128 ? 2 : 4) : 0;
   k.T = k.NT > 0 ? 8 * k.NT : 128;

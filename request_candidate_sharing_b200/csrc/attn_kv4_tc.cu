@@ -11,8 +11,8 @@
 //   warps 4-6  (and 8-10 with d = 64 or 128) producers: a thread takes one group (16 bytes of codes and
 //              their scale) of a key or a value at a time, a block ahead in registers, dequantises it
 //              (exactly) and writes it as bf16 into the operand's swizzled tile in shared memory.  The
-//              conversion is paid once per 128 rows; a copy of the codes through shared memory would only
-//              lengthen the way.
+//              conversion is paid once per 128 rows.  (Codes by bulk copies several blocks ahead, as the
+//              kernel for few rows has them, are not tried here.)
 //   warp 7     issues the MMAs: S_j = Q K_j^T into one of two buffers, O += P_j V_j.  They execute in
 //              order, so S_{j+1} is there when the softmax is done with S_j, and the P in a buffer is
 //              consumed before the S two blocks later lands on it: one wait and one arrival a block.
@@ -21,12 +21,15 @@
 // stored.  All waits are bounded (ROCS_ERR_DEVICE_TIMEOUT), after which the CTA drains its MMAs, releases
 // tensor memory and returns.
 //
-// Bound by the softmax: the exponential unit is about 61% busy while blocks are full, the rest are the
-// latencies of barriers and tensor memory between its turns.  41388 candidates of 96 requests (8 heads of
-// 32, 675 keys a request on average) take 123 us, of which the exponentials alone are 39 and the products 17;
-// 7601 causal rows of 48 requests (4 heads of 64 shared by two query heads, 2200 keys) 106 us, of 22
-// and 19.
-// Tried and slower there: exponentials by polynomial for 1/8 to 3/8 of the elements (1 to 5%), loads two
+// Weights enter the product as bf16, and their sum is of those: a value that all keys share comes out as it
+// is.  Two bf16 numbers a weight would leave the output's rounding alone (1.65e-3 of the result instead of
+// 2.2e-3) for 142 and 120 us below.
+// No unit is full: 41388 candidates of 96 requests (8 heads of 32, 675 keys a request on average) take 129 us
+// with the exponential unit 43% and the issue slots 55% busy, and the exponentials alone would take 39 and the
+// products 17.  A third is the CTAs' start and end, the rest latency between the roles; without exponentials it
+// took 6 us less, without the conversion 2, without both 14.  7601 causal rows of 48 requests (4 heads of
+// 64 shared by two query heads, 2200 keys) 109 us, of 22 and 19.
+// Tried and slower, when these took 123 and 106: exponentials by polynomial for 1/8 to 3/8 of the elements (1 to 5%), loads two
 // blocks ahead (145 and 122 us), blocks of 32 keys with four CTAs an SM (124 and 138), three CTAs of one S
 // buffer with d = 64 (146 against 139 then), heads outside tiles in the order of blocks (135 and 133),
 // keys split where blocks are about as many as slots (no gain).

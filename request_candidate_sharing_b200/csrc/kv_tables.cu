@@ -13,7 +13,7 @@
 // Up to kTabInline requests every block computes both totals by itself in shared memory (two reads of
 // 4 B a request from L2, one block-wide scan): one launch instead of three.  A decode step (512 requests,
 // 512 rows) is all latency: with at most four rows a request on average one block does it all without a
-// search, 3.6 us, where the form below takes 9.7 us.
+// search, 3.7 us, where the form below takes 9.7 us.
 // Beyond, a block per kTabThreads requests totals its part, a second launch scans and writes the totals,
 // a third expands.  Expansion is by output row, so that one request with a million rows spreads over the
 // whole GPU.  A block takes a tile of neighbouring rows, finds its first request by two block-wide probes,

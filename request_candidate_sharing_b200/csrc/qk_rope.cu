@@ -6,16 +6,17 @@
 // (2 t, 2 t + 1) when pairs are neighbours.  fp32 inside, one rounding at the end.
 //
 // Bound by memory: every element is read and written once; but only if an element costs few
-// instructions (at 6.5 TB/s an SM has about 20 issue slots per eight bf16 elements).  So a lane keeps
+// instructions (at 6.5 TB/s there are about 177 issue slots of a lane per eight bf16 elements, and about 127
+// are taken).  So a lane keeps
 // four whole pairs of a head: with half-split pairs elements 4 l .. 4 l + 3 and their partners d_rot / 2
 // further on, no shuffles; else (neighbouring pairs, or past d_rot) eight neighbours.  A head is d / 8
 // lanes of one warp, the mean a few shuffles, a warp covers 32 / lanes heads of a row at a time; the
 // arithmetic is on packed fp32 pairs, and lanes past d_rot turn by nothing.
 // A warp takes a few (row, unit of heads) items of the queries or of the keys, and asks for their
 // elements, positions and then angles before it works on the first; nothing loops, so that the registers
-// allow many warps.  For 524288 rows of 8 + 8 heads of 32: 190 us (87% of the measured copy bandwidth);
+// allow many warps.  For 524288 rows of 8 + 8 heads of 32: 193 us (85% of the measured copy bandwidth);
 // 295 us where warps walked over many rows with the next elements in flight, 253 us where each item
-// chose its side.  fp32, 30011 rows of 16 + 2 heads of 128: 91 us (94%).
+// chose its side.  fp32, 30011 rows of 16 + 2 heads of 128: 92 us (94%).
 #include "common.cuh"
 #include "internal.h"
 
@@ -277,8 +278,8 @@ rocs_status launch_qk_norm_rope(rocs_context* ctx, const rocs_qk_desc& d, const 
   for (QkSide& sd : p.side) sd.units = (sd.H + heads - 1) / heads;
   p.full = d.d_h == 8 * T && d.d_rot == d.d_h;
   // One item a warp until the warps fill the GPU (1.7 instead of 2.2 us on 512 rows), then several: bf16 three
-  // and four blocks an SM where the head is full (190 us on 524288 rows of 16 heads of 32, four and three
-  // 201), else four and three (131072 rows of 20 heads of 128 of which 64 turn: 286 us, three and three 297).
+  // and four blocks an SM where the head is full (193 us on 524288 rows of 16 heads of 32, four and three
+  // 11 more), else four and three (131072 rows of 20 heads of 128 of which 64 turn: 286 us, three and three 297).
   const long long all = d.rows * (p.side[0].units + p.side[1].units);
   p.items = all < 48LL * ctx->num_sms ? 1
             : d.io != ROCS_BF16       ? (p.full ? QkRaw<float>::ITEMS : QkRaw<float>::ITEMS_PARTIAL)
