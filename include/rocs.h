@@ -438,7 +438,7 @@ rocs_status rocs_kv4_gather(rocs_handle_t handle, const rocs_kv4_desc* desc, con
  *     what is written for them is no result.
  *   O [rows, H_q * d_h] bf16, row stride ld_O: softmax(q k^T * scale) v; a row that sees no key is 0.
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights enter the second product as
- * bf16.  Offsets that decrease or leave [0, rows] set ROCS_ERR_INDEX, a kv_len outside its range
+ * bf16, and their sum is of the rounded ones.  Offsets that decrease or leave [0, rows] set ROCS_ERR_INDEX, a kv_len outside its range
  * ROCS_ERR_COUNTS: those requests' rows are not written (and where offsets go back, other requests' rows
  * may not be written either).  A needed page outside [0, n_pages) sets ROCS_ERR_INDEX;
  * its keys are left out.  Rows behind the last request's are left as they were.
